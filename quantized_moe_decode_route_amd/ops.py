@@ -42,6 +42,13 @@ class _Worklist(ctypes.Structure):
                 ("seg", ctypes.c_void_p), ("assign", ctypes.c_void_p)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("data", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("ref", ctypes.c_void_p)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -71,6 +78,17 @@ for _b in ("q4", "q8", "q2"):
                                            _I)
     _SIGS[f"moe_layer_fused_resid_{_b}"] = ([_P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _F, _P, _P, _P, _P, _P, _P, _P,
                                              _P, _P], _I)
+    _SIGS[f"dense_linear_{_b}"] = ([_P, _I, _I64, _P, _P, _P, _I, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P],
+                                   _I)
+_SIGS["dense_linear_workspace"] = ([_I, _I64, _I64], _I64)
+_SIGS["kv4_append"] = ([_P, _I, _P, _I64, _P, _I64, _I, _I64, _P, _P, _P], _I)
+_SIGS["kv4_read"] = ([_P, _I, _P, _P, _I64, _P, _I64, _P, _I64, _I, _P], _I)
+_SIGS["kv4_attention_workspace"] = ([_P, _I64, _I, _I64], _I64)
+_SIGS["kv4_attention"] = ([_P, _I, _P, _I64, _I, _I64, _I, _P, _P, _F, _I, _I64, _P, _I64, _P, _P, _I64, _P], _I)
+_SIGS["kv4_reserve"] = ([_P, _P, _P, _P, _P], _I)
+_SIGS["kv4_fork"] = ([_P, _I, _P, _P, _P, _P, _P], _I)
+_SIGS["kv4_truncate"] = ([_P, _P, _P], _I)
+_SIGS["kv4_compact"] = ([_P, _P, _P, _P, _P], _I)
 _SIGS["moe_expert_down_combine_em_noalloc_q4"] = ([_P, _P, _P, _P, _P, _I, _I, _P, _P], _I)
 
 MOEDEC_ERR_UNSUPPORTED = 2
@@ -376,6 +394,258 @@ def residual_rmsnorm(x: torch.Tensor, y: torch.Tensor | None, xn: torch.Tensor, 
     st = lib().moe_residual_rmsnorm(_dev(x, torch.float32, "x"), yp, _dev(xn, torch.float32, "xn"), T, H,
                                     float(eps), _stream(x))
     _check("moe_residual_rmsnorm", st)
+
+
+# ------------------------------------------------- the attention half of a layer
+#
+# The calls of include/moedec_attn.h.  Tensors may live on any one GPU (not only
+# the current one); work goes to that GPU's current stream.
+
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
+KV4_MAX_SEQS = 1024
+
+
+def _launch(name: str, dev: torch.device, *args) -> None:
+    """The call on dev's current stream (its last argument), dev made current."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(name, st)
+
+
+def _rows(t: torch.Tensor, inner: tuple, name: str, dev: torch.device) -> tuple[int, int]:
+    """Pointer and row stride of rows [n, *inner], each row contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be on {dev} (a GPU)")
+    if t.dtype not in DTYPES:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if t.dim() != 1 + len(inner) or tuple(t.shape[1:]) != inner:
+        raise ValueError(f"{name} must be [rows, {', '.join(map(str, inner))}], got {tuple(t.shape)}")
+    row, need = 1, t.stride()
+    for i in range(len(inner), 0, -1):
+        if inner[i - 1] != 1 and need[i] != row:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        row *= inner[i - 1]
+    return t.data_ptr(), (need[0] if t.shape[0] > 1 else row)
+
+
+def _on(t: torch.Tensor, dtype: torch.dtype, name: str, dev: torch.device, shape: tuple) -> int:
+    p = _dev(t, dtype, name)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return p
+
+
+@dataclass
+class Linear:
+    """A packed weight: codes as ops.pack / ops.quantize_rows(pack=True) write them."""
+    q: torch.Tensor                     # uint8 [N, K*bits/8]
+    scale: torch.Tensor                 # fp32 [N]
+    bits: int
+    bias: torch.Tensor | None = None    # fp32 [N]
+
+    @property
+    def n_in(self) -> int:
+        return self.q.shape[1] * 8 // self.bits
+
+    @property
+    def n_out(self) -> int:
+        return self.q.shape[0]
+
+
+def linear(x: torch.Tensor, lin: Linear, act: str = "none", residual: torch.Tensor | None = None,
+           out: torch.Tensor | None = None) -> torch.Tensor:
+    """dense_linear_q{bits}: act(x W^T + bias) + residual for rows x [T, K] of
+    float32, float16 or bfloat16; out and residual [T, N] of the same type (out
+    may be residual).  act: none, silu, gelu (erf), relu."""
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    suffix, dev = _suffix(lin.bits), x.device
+    K, N = lin.n_in, lin.n_out
+    xp, ldx = _rows(x, (K,), "x", dev)
+    T = x.shape[0]
+    if out is None:
+        out = torch.empty((T, N), dtype=x.dtype, device=dev)
+    yp, ldy = _rows(out, (N,), "out", dev)
+    rp, ldr = (None, 0) if residual is None else _rows(residual, (N,), "residual", dev)
+    if out.dtype != x.dtype or (residual is not None and residual.dtype != x.dtype):
+        raise ValueError("x, residual and out must have one dtype")
+    if out.shape[0] != T or (residual is not None and residual.shape[0] != T):
+        raise ValueError("residual and out must have x's rows")
+    wp = _on(lin.q, torch.uint8, "q", dev, (N, lin.q.shape[1]))
+    sp = _on(lin.scale, torch.float32, "scale", dev, (N,))
+    bp = None if lin.bias is None else _on(lin.bias, torch.float32, "bias", dev, (N,))
+    dt = DTYPES[x.dtype]
+    nb = lib().dense_linear_workspace(dt, T, K)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb > 0 else None
+    _launch(f"dense_linear_{suffix}", dev, xp, dt, ldx, wp, sp, bp, ACTS[act], rp, ldr, yp, ldy, T, K, N,
+            ws.data_ptr() if nb > 0 else None, max(nb, 0))
+    return out
+
+
+@dataclass
+class KvCache:
+    """A paged cache of keys and values in 4 bits (see kv4_cache).  One table of
+    pages serves all layers; the page calls keep table, len and ref on the GPU."""
+    data: torch.Tensor    # uint8 [layers, n_pages, kv_heads * page_tokens * (head_dim + 8)]
+    table: torch.Tensor   # int32 [n_seqs, max_pages]
+    len: torch.Tensor     # int32 [n_seqs]
+    ref: torch.Tensor     # int32 [n_pages]
+    page_tokens: int
+    kv_heads: int
+    head_dim: int
+
+    @staticmethod
+    def allocate(layers: int, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int, n_seqs: int,
+                 max_pages: int, device) -> "KvCache":
+        """An empty cache (the pages' contents are not initialised)."""
+        z = dict(dtype=torch.int32, device=device)
+        data = torch.empty((layers, n_pages, kv_heads * page_tokens * (head_dim + 8)), dtype=torch.uint8,
+                           device=device)
+        return KvCache(data, torch.full((n_seqs, max_pages), -1, **z), torch.zeros(n_seqs, **z),
+                       torch.zeros(n_pages, **z), page_tokens, kv_heads, head_dim)
+
+    @property
+    def layers(self) -> int:
+        return self.data.shape[0]
+
+    @property
+    def n_pages(self) -> int:
+        return self.data.shape[1]
+
+    @property
+    def n_seqs(self) -> int:
+        return self.table.shape[0]
+
+    @property
+    def max_pages(self) -> int:
+        return self.table.shape[1]
+
+    @property
+    def device(self) -> torch.device:
+        return self.data.device
+
+    def struct(self) -> _KvCache:
+        dev, (L, P, nb), (S, mp) = self.device, self.data.shape, self.table.shape
+        if nb != self.kv_heads * self.page_tokens * (self.head_dim + 8):
+            raise ValueError(f"data has {nb} bytes a page, expected kv_heads * page_tokens * (head_dim + 8)")
+        return _KvCache(L, P, self.page_tokens, self.kv_heads, self.head_dim, S, mp,
+                        _on(self.data, torch.uint8, "data", dev, (L, P, nb)),
+                        _on(self.table, torch.int32, "table", dev, (S, mp)),
+                        _on(self.len, torch.int32, "len", dev, (S,)), _on(self.ref, torch.int32, "ref", dev, (P,)))
+
+    def _ints(self, t: torch.Tensor | None, name: str, n: int) -> int | None:
+        return None if t is None else _on(t, torch.int32, name, self.device, (n,))
+
+
+def kv4_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
+               granted: torch.Tensor | None = None) -> None:
+    """kv4_append: rows q_start[s] .. q_start[s+1]-1 of k and v [rows, kv_heads,
+    head_dim] become the last positions of sequence s (len[s] already counts
+    them; granted: what kv4_reserve gave)."""
+    c, dev, inner = cache.struct(), cache.device, (cache.kv_heads, cache.head_dim)
+    kp, ldk = _rows(k, inner, "k", dev)
+    vp, ldv = _rows(v, inner, "v", dev)
+    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have one dtype and as many rows")
+    _launch("kv4_append", dev, ctypes.byref(c), layer, kp, ldk, vp, ldv, DTYPES[k.dtype], k.shape[0],
+            cache._ints(q_start, "q_start", cache.n_seqs + 1), cache._ints(granted, "granted", cache.n_seqs))
+
+
+def kv4_read(cache: KvCache, layer: int, first: torch.Tensor, q_start: torch.Tensor, rows: int,
+             dtype: torch.dtype = torch.float32) -> tuple[torch.Tensor, torch.Tensor]:
+    """kv4_read: the values of positions first[s] .. of sequence s in rows
+    q_start[s] .. q_start[s+1]-1 of k and v [rows, kv_heads, head_dim]."""
+    c, dev = cache.struct(), cache.device
+    if dtype not in DTYPES:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    k, v = (torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev) for _ in range(2))
+    ld = cache.kv_heads * cache.head_dim
+    _launch("kv4_read", dev, ctypes.byref(c), layer, cache._ints(first, "first", cache.n_seqs),
+            cache._ints(q_start, "q_start", cache.n_seqs + 1), rows, k.data_ptr(), ld, v.data_ptr(), ld,
+            DTYPES[dtype])
+    return k, v
+
+
+def kv4_attention(q: torch.Tensor, cache: KvCache, layer: int, q_start: torch.Tensor, *, scale: float | None = None,
+                  window: int = 0, granted: torch.Tensor | None = None, max_len: int | None = None,
+                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None) -> torch.Tensor:
+    """kv4_attention: causal attention of the queries q [rows, heads, head_dim],
+    the last positions of their sequences, over the cache; returns out (rows of
+    no sequence are left as they are).  scale defaults to head_dim^-0.5; window >
+    0 keeps the last window keys of each query; max_len: an upper bound of the
+    lengths, where the caller knows one (it sizes the launch only); lse: fp32
+    [rows, heads] to fill with the log-sum-exp of the scores."""
+    c, dev = cache.struct(), cache.device
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, heads, head_dim]")
+    rows, heads = q.shape[0], q.shape[1]
+    qp, ldq = _rows(q, (heads, cache.head_dim), "q", dev)
+    if out is None:
+        out = torch.empty((rows, heads, cache.head_dim), dtype=q.dtype, device=dev)
+    op, ldo = _rows(out, (heads, cache.head_dim), "out", dev)
+    if out.dtype != q.dtype or out.shape[0] != rows:
+        raise ValueError("out must have q's dtype and rows")
+    lp = None if lse is None else _on(lse, torch.float32, "lse", dev, (rows, heads))
+    cap = cache.max_pages * cache.page_tokens
+    bound = cap if max_len is None else min(int(max_len), cap)
+    nb = lib().kv4_attention_workspace(ctypes.byref(c), rows, heads, bound)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb > 0 else None
+    _launch("kv4_attention", dev, ctypes.byref(c), layer, qp, ldq, DTYPES[q.dtype], rows, heads,
+            cache._ints(q_start, "q_start", cache.n_seqs + 1), cache._ints(granted, "granted", cache.n_seqs),
+            cache.head_dim ** -0.5 if scale is None else float(scale), window, bound, op, ldo, lp,
+            ws.data_ptr() if nb > 0 else None, max(nb, 0))
+    return out
+
+
+def kv4_reserve(cache: KvCache, n_new: torch.Tensor) -> torch.Tensor:
+    """kv4_reserve: len += n_new (int32 [n_seqs]) with pages for the new tokens,
+    shared partly filled pages copied first; returns granted (n_new, or 0 where
+    there was no room and nothing changed)."""
+    c, dev, S = cache.struct(), cache.device, cache.n_seqs
+    granted = torch.empty(S, dtype=torch.int32, device=dev)
+    ws = torch.empty(2 * S + 1, dtype=torch.int32, device=dev)
+    _launch("kv4_reserve", dev, ctypes.byref(c), cache._ints(n_new, "n_new", S), granted.data_ptr(), ws.data_ptr())
+    return granted
+
+
+def kv4_fork(cache: KvCache, src: torch.Tensor, dst: torch.Tensor,
+             n_tokens: torch.Tensor | None = None) -> torch.Tensor:
+    """kv4_fork: the empty slots dst[i] become branches of src[i] (its first
+    n_tokens[i] tokens) that share its pages; returns ok (int32, 1 or 0)."""
+    c, dev, n = cache.struct(), cache.device, src.shape[0]
+    ok = torch.empty(n, dtype=torch.int32, device=dev)
+    _launch("kv4_fork", dev, ctypes.byref(c), n, cache._ints(src, "src", n), cache._ints(dst, "dst", n),
+            cache._ints(n_tokens, "n_tokens", n), ok.data_ptr())
+    return ok
+
+
+def kv4_truncate(cache: KvCache, new_len: torch.Tensor) -> None:
+    """kv4_truncate: sequence s keeps its first new_len[s] tokens (negative:
+    untouched, 0: freed); pages nothing holds any more become free."""
+    c = cache.struct()
+    _launch("kv4_truncate", cache.device, ctypes.byref(c), cache._ints(new_len, "new_len", cache.n_seqs))
+
+
+def kv4_compact(cache: KvCache) -> tuple[torch.Tensor, torch.Tensor]:
+    """kv4_compact: live pages move to the front of the pool; returns (remap
+    int32 [n_pages]: new index of every page or -1, n_live int32 [1])."""
+    c, dev, P = cache.struct(), cache.device, cache.n_pages
+    remap = torch.empty(P, dtype=torch.int32, device=dev)
+    live = torch.empty(1, dtype=torch.int32, device=dev)
+    ws = torch.empty(P + 1, dtype=torch.int32, device=dev)
+    _launch("kv4_compact", dev, ctypes.byref(c), remap.data_ptr(), live.data_ptr(), ws.data_ptr())
+    return remap, live
 
 
 # ------------------------------------------------------------- a whole layer
