@@ -7,6 +7,11 @@
 // pair of fp16 (about 22 bits), two MFMAs instead of one.  The power of two, the
 // row scale, bias, activation and residual are applied once, in fp32, to the
 // sums.
+//
+// Weight rows are the M side (A operand: lane l holds row l % 16), tokens the N
+// side.  A wave turns the packed codes into fp16 in its own registers: at 2 to 8
+// bits they are a small fraction of the bytes, so they go from global memory
+// straight to the lanes and only the activations pass through LDS.
 #include "attn.h"
 #include "mfma.h"
 
@@ -18,61 +23,26 @@ namespace {
 using mfma::a_operand;
 using mfma::MfmaCodec;
 
-constexpr int kPad = 256;                 // columns a plane's row is padded to (a chunk of 2-bit codes)
 constexpr int kPrepThreads = 256;
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+constexpr int kStage = 4;                 // MFMA calls (of 32 columns) of a staged step
+constexpr float kFltMax = 3.402823466e38f;
 
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }
 
 // Exponent k with m * 2^k in [2^14, 2^15) (0 for zero and non-finite m).
 __device__ __forceinline__ int row_exponent(float m) {
-    if (!(m > 0.f) || !(m <= 3.402823466e38f)) return 0;
+    if (!(m > 0.f) || !(m <= kFltMax)) return 0;
     const int k = 14 - ((int)(__float_as_uint(m) >> 23) - 127);
     return k > 120 ? 120 : k;
 }
 
-__host__ __device__ inline int64_t padded(int64_t K) { return (K + kPad - 1) / kPad * kPad; }
-
-// A row of x as fp16 planes (hi, and lo for fp32), its columns in the order the
-// codes of a 16-byte group enter the MFMAs, zero past K; inv = 2^-k of the row.
-template <typename T, int BITS>
-__global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T::type* __restrict__ x, int64_t ldx,
-                                                               int K, int Kp, _Float16* __restrict__ hi,
-                                                               _Float16* __restrict__ lo, float* __restrict__ inv) {
-    using M = MfmaCodec<BITS>;
-    constexpr int CW = 128 / BITS;
-    const int64_t t = blockIdx.x;
-    const typename T::type* row = x + t * ldx;
-    __shared__ float red[kPrepThreads / kWave];
-    float m = 0.f;
-    for (int c = threadIdx.x * 8; c < K; c += kPrepThreads * 8) {
-        float v[8];
-        load8<T>(row + c, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
-    }
-    m = wave_max(m);
-    if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const int k = row_exponent(m);
-    const float f = pow2(k);
-    if (threadIdx.x == 0) inv[t] = pow2(-k);
-    for (int c = threadIdx.x * 8; c < Kp; c += kPrepThreads * 8) {
-        half8 h, l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int col = c / CW * CW + M::col(c % CW / 8, e);
-            const float v = col < K ? T::get(row[col]) : 0.f;
-            const mfma::F16Pair p = mfma::split_f16(v, f);
-            h[e] = p.hi;
-            l[e] = p.lo;
-        }
-        *reinterpret_cast<half8*>(hi + t * Kp + c) = h;
-        if (T::bytes == 4) *reinterpret_cast<half8*>(lo + t * Kp + c) = l;
-    }
+// Columns a plane's row is padded to: whole 64-byte chunks of codes (4 groups of
+// 16 bytes, one per lane of a row) and whole staged steps.
+__host__ __device__ constexpr int pad_of(int bits) { return bits == 2 ? 256 : 128; }
+__host__ __device__ inline int64_t padded(int64_t K, int bits) {
+    return (K + pad_of(bits) - 1) / pad_of(bits) * pad_of(bits);
 }
+__host__ __device__ inline int64_t blocks16(int64_t T) { return (T + 15) / 16; }
 
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
@@ -83,63 +53,528 @@ __device__ __forceinline__ float activate(float v, int act) {
     }
 }
 
-// 16 weight rows by 16 tokens a workgroup, its waves splitting K.
-template <typename T, int BITS>
-__global__ __launch_bounds__(kThreads) void linear_simple(LinearArgs a, int Kp, const _Float16* __restrict__ hi,
-                                                          const _Float16* __restrict__ lo,
-                                                          const float* __restrict__ inv) {
+// Row scale and bias of four consecutive rows r .. r+3, loaded ahead of the sums.
+struct Params {
+    float scale[4], bias[4];
+};
+__device__ __forceinline__ Params load_params(const LinearArgs& a, int r) {
+    Params p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = min(r + i, a.N - 1);
+        p.scale[i] = a.scale[n];
+        p.bias[i] = a.bias ? a.bias[n] : 0.f;
+    }
+    return p;
+}
+
+// The epilogue of rows r .. r+3 of token t; `whole`: y is aligned for one store
+// of four outputs.
+template <typename T>
+__device__ __forceinline__ void finish4(const LinearArgs& a, int t, int r, float inv, const floatx4& sum,
+                                        const Params& p, bool whole) {
+    if (r >= a.N) return;
+    typename T::type* y = reinterpret_cast<typename T::type*>(a.y) + (int64_t)t * a.ldy + r;
+    const typename T::type* res = reinterpret_cast<const typename T::type*>(a.residual) + (int64_t)t * a.ldr + r;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = sum[i] * inv * p.scale[i];
+        if (a.bias) v[i] += p.bias[i];
+        v[i] = activate(v[i], a.act);
+    }
+    if (whole && r + 3 < a.N) {
+        if (a.residual) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += T::get(res[i]);
+        }
+        store4<T>(y, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (r + i >= a.N) break;
+        if (a.residual) v[i] += T::get(res[i]);
+        y[i] = T::put(v[i]);
+    }
+}
+
+// ---------------------------------------------------------- units of a row
+//
+// A unit is the 8 columns that one lane group (0 .. 3) supplies to one call: two
+// pieces of 4 consecutive columns, interleaved as a_operand orders the codes.
+
+template <typename T>
+__device__ __forceinline__ void load4(const typename T::type* p, float* o) {
+    if constexpr (T::bytes == 4) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = a[i];
+    } else {
+        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+        const u16x4 a = *reinterpret_cast<const u16x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = T::get(__builtin_bit_cast(typename T::type, (uint16_t)a[i]));
+    }
+}
+
+// First columns of the two pieces of unit u = call * 4 + group.  K is a multiple
+// of a 16-byte group's columns, so a unit lies inside the row or past its end.
+template <int BITS>
+__device__ __forceinline__ void unit_cols(int u, int& c0, int& c1) {
     using M = MfmaCodec<BITS>;
-    constexpr int CW = 128 / BITS;
+    const int q = u >> 2, c = q % M::NCALL, col0 = (q / M::NCALL * 4 + (u & 3)) * (128 / BITS);
+    c0 = col0 + M::col(c, 0);
+    c1 = c0 + (BITS == 2 ? 8 : 4);
+}
+template <typename T, int BITS>
+__device__ __forceinline__ void load_unit(const typename T::type* row, int K, int u, float* v) {
+    int c0, c1;
+    unit_cols<BITS>(u, c0, c1);
+    if (c0 < K) {
+        load4<T>(row + c0, v);
+        load4<T>(row + c1, v + 4);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+}
+// Piece element of operand element e.
+template <int BITS>
+__device__ __forceinline__ constexpr int unit_element(int e) {
+    return BITS == 8 ? 4 * (e >> 2) + ((e >> 1) & 1) + 2 * (e & 1) : (e >> 1) + 4 * (e & 1);
+}
+template <int BITS>
+__device__ __forceinline__ void split_unit(const float* v, float f, half8& hi, half8& lo) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const mfma::F16Pair p = mfma::split_f16(v[unit_element<BITS>(e)], f);
+        hi[e] = p.hi;
+        lo[e] = p.lo;
+    }
+}
+
+__device__ __forceinline__ float max8(const float* v, float m) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+    return m;
+}
+
+// ------------------------------------------------------- activations as planes
+
+// A plane holds fp16 activations in the order the B operand of the MFMAs takes
+// them: [16 tokens][call of 32 columns][lane][8], 1 KB a call, so every later
+// load of it is linear.  Call q of chunk c multiplies the columns that a_operand
+// gives for call q of a 16-byte group of codes.
+//
+// One wave a token.  Rows of up to 512 * NU columns stay in registers between the
+// pass for the largest magnitude and the conversion (NU = 0: read twice).
+// HBM-bound: x read once, the planes written once; the 16 bytes a lane stores
+// meet those of the block's other tokens in the L2 of one XCD.
+template <typename T, int BITS, int NU>
+__global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T::type* __restrict__ x, int64_t ldx,
+                                                               int T_, int K, int calls, half8* __restrict__ hi,
+                                                               half8* __restrict__ lo, float* __restrict__ inv) {
+    const int lane = threadIdx.x & (kWave - 1);
+    // the waves of a block of 16 tokens run on one XCD (workgroups go to the XCDs round robin)
+    constexpr int kParts = 16 / (kPrepThreads / kWave);
+    const int xcd = blockIdx.x % 8, i8 = blockIdx.x / 8;
+    const int64_t block = (int64_t)(i8 / kParts) * 8 + xcd;
+    const int n = i8 % kParts * (kPrepThreads / kWave) + threadIdx.x / kWave;
+    const int64_t t = block * 16 + n;
+    if (block * 16 >= T_) return;
+    const bool on = t < T_;
+    const typename T::type* row = x + (on ? t : 0) * ldx;
+    const int units = calls * 4, cols = on ? K : 0;
+    auto put = [&](int u, const float* v, float f) {
+        half8 h, l;
+        split_unit<BITS>(v, f, h, l);
+        const int64_t at = (block * calls + (u >> 2)) * kWave + (u & 3) * 16 + n;
+        hi[at] = h;
+        if (T::bytes == 4) lo[at] = l;
+    };
+    float m = 0.f;
+    if constexpr (NU > 0) {
+        float v[NU][8];
+#pragma unroll
+        for (int i = 0; i < NU; ++i) load_unit<T, BITS>(row, lane + i * kWave < units ? cols : 0, lane + i * kWave, v[i]);
+#pragma unroll
+        for (int i = 0; i < NU; ++i) m = max8(v[i], m);
+        m = wave_max(m);
+        const float f = pow2(row_exponent(m));
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+            if (lane + i * kWave < units) put(lane + i * kWave, v[i], f);
+    } else {
+        float v[8];
+        for (int u = lane; u < units; u += kWave) {
+            load_unit<T, BITS>(row, cols, u, v);
+            m = max8(v, m);
+        }
+        m = wave_max(m);
+        const float f = pow2(row_exponent(m));
+        for (int u = lane; u < units; u += kWave) {
+            load_unit<T, BITS>(row, cols, u, v);
+            put(u, v, f);
+        }
+    }
+    if (lane == 0) inv[t] = pow2(-row_exponent(m));
+}
+
+// ------------------------------------------------------------- many tokens
+
+typedef __attribute__((address_space(1))) const void* gptr_t;
+typedef __attribute__((address_space(3))) void* lptr_t;
+
+// A packed step of one 16-row block: the words of kStage consecutive calls.
+template <int BITS>
+struct Packed {
+    uint32_t w[BITS];                    // 4 calls * 8 codes * BITS / 32 words
+};
+template <int BITS>
+__device__ __forceinline__ Packed<BITS> load_packed(const uint8_t* tile, uint32_t row, int groups, int s, int g) {
+    Packed<BITS> p;
+    auto at = [&](int gr) { return tile + (row + (uint32_t)min(gr, groups - 1) * 16u); };
+    if constexpr (BITS == 4) {
+        const uint4 q = ld16(at(4 * s + g));
+        p.w[0] = q.x, p.w[1] = q.y, p.w[2] = q.z, p.w[3] = q.w;
+    } else if constexpr (BITS == 8) {
+        const uint4 q = ld16(at(8 * s + g));
+        const uint4 r = ld16(at(8 * s + 4 + g));
+        p.w[0] = q.x, p.w[1] = q.y, p.w[2] = q.z, p.w[3] = q.w;
+        p.w[4] = r.x, p.w[5] = r.y, p.w[6] = r.z, p.w[7] = r.w;
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(at(4 * (s >> 1) + g) + 8 * (s & 1));
+        p.w[0] = q.x, p.w[1] = q.y;
+    }
+    return p;
+}
+// The A operand of call c (0 .. 3) of a packed step.
+template <int BITS>
+__device__ __forceinline__ half8 step_operand(const Packed<BITS>& p, int c) {
+    if constexpr (BITS == 4) return a_operand<4>(uint4{p.w[0], p.w[1], p.w[2], p.w[3]}, c);
+    else if constexpr (BITS == 8)
+        return a_operand<8>(uint4{p.w[4 * (c >> 1)], p.w[4 * (c >> 1) + 1], p.w[4 * (c >> 1) + 2],
+                                  p.w[4 * (c >> 1) + 3]}, c & 1);
+    else return a_operand<2>(uint4{p.w[0], p.w[1], 0, 0}, c);
+}
+
+// Workgroup tile: WN * NB * 16 weight rows by WT * TB * 16 tokens, WN x WT waves.
+// Per step of 128 columns the activations (WT * TB * 4 KB) go to one of two LDS
+// buffers by direct loads while the other is multiplied; each wave keeps the next
+// step's packed codes in registers.  One barrier a step.  fp32: a step is 64
+// columns of both planes, each converted code used twice.
+//
+// Bound by the matrix cores: a wave's step is 4 * NB * TB MFMAs of 16 cycles
+// against 4 * NB conversions of 9 vector instructions.  Workgroups are dealt to
+// the eight XCDs in contiguous runs of tiles, four token tiles by the weight
+// tiles, so that an XCD's L2 serves each activation tile to several workgroups.
+template <typename T, int BITS, int NB, int TB, int WN, int WT>
+__global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, const half8* __restrict__ hi,
+                                                               const half8* __restrict__ lo,
+                                                               const float* __restrict__ inv, int calls, bool whole) {
+    constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
+    constexpr int kW = WN * WT;
+    constexpr int kLoads = WT * TB * kStage / kW;          // 1 KB direct loads a wave makes per step
+    static_assert(WT * TB * kStage % kW == 0, "direct loads divide over the waves");
+    __shared__ half8 buf[2][WT * TB * kStage * kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int n = lane & 15, g = lane >> 4, wn = wave % WN, wt = wave / WN;
+    const int tiles_n = (a.N + WN * NB * 16 - 1) / (WN * NB * 16), tiles_t = (a.T + WT * TB * 16 - 1) / (WT * TB * 16);
+    const int total = tiles_n * tiles_t, per = (total + 7) / 8;
+    const int id = blockIdx.x % 8 * per + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= per || id >= total) return;
+    const int band = id / (4 * tiles_n), in = id % (4 * tiles_n), high = min(tiles_t - 4 * band, 4);
+    const int tile_t = 4 * band + in % high, tile_n = in / high;
+    const int r0 = (tile_n * WN + wn) * NB * 16, tb0 = tile_t * WT * TB, last_tb = (int)blocks16(a.T) - 1;
+    const int groups = a.K / (128 / BITS), steps = calls / kStage;
+    // the tile's rows by 32-bit offsets (at most 256 rows of 64 KB)
+    const int tr0 = tile_n * WN * NB * 16;
+    const uint8_t* wtile = a.w + (int64_t)tr0 * groups * 16;
+    uint32_t wrow[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) wrow[b] = (uint32_t)(min(r0 + 16 * b + n, a.N - 1) - tr0) * (uint32_t)(groups * 16);
+
+    // LDS unit k (0 .. 3) of a token block: call k, or (fp32) plane k / 2 of call k % 2
+    auto stage = [&](int s, int to) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int u = wave * kLoads + i;                               // (token block, call)
+            const int tb = min(tb0 + u / kStage, last_tb);
+            const int k = u % kStage;
+            const half8* src = (kPlanes == 2 && k >= 2 ? lo : hi) +
+                               ((int64_t)tb * calls + (kPlanes == 2 ? 2 * s + (k & 1) : kStage * s + k)) * kWave + lane;
+            __builtin_amdgcn_global_load_lds((gptr_t)src, (lptr_t)&buf[to][u * kWave], 16, 0, 0);
+        }
+    };
+
+    floatx4 acc[NB][TB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[b][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+    Packed<BITS> next[NB], cur[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) next[b] = load_packed<BITS>(wtile, wrow[b], groups, 0, g);
+    stage(0, 0);
+    for (int p = 0; p < steps; ++p) {                      // 128 columns: one packed step
+#pragma unroll
+        for (int h = 0; h < kPlanes; ++h) {
+            const int s = p * kPlanes + h;
+            __syncthreads();                               // step s is in LDS, step s - 1 is done with
+            if (h == 0) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) cur[b] = next[b];
+            }
+            if (s + 1 < steps * kPlanes) stage(s + 1, (s + 1) & 1);
+            if (h == 0 && p + 1 < steps) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) next[b] = load_packed<BITS>(wtile, wrow[b], groups, p + 1, g);
+            }
+            const half8* x = buf[s & 1] + wt * TB * kStage * kWave + lane;
+#pragma unroll
+            for (int c = 0; c < kStage / kPlanes; ++c) {
+                half8 w[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) w[b] = step_operand<BITS>(cur[b], kPlanes == 2 ? 2 * h + c : c);
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+#pragma unroll
+                    for (int k = c; k < kStage; k += kStage / kPlanes) {
+                        const half8 v = x[(t * kStage + k) * kWave];
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) acc[b][t] = mfma::mfma(w[b], v, acc[b][t]);
+                    }
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int r = r0 + 16 * b + 4 * g;
+        const Params par = load_params(a, r);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            const int tok = (tb0 + wt * TB + t) * 16 + n;
+            if (tok < a.T) finish4<T>(a, tok, r, inv[tok], acc[b][t], par, whole);
+        }
+    }
+}
+
+// ------------------------------------------------------------- some tokens
+//
+// Up to TB * 16 tokens: bound by the weights' bytes (and, from some 30 tokens on,
+// by the planes' L2 reads).  A workgroup owns 16 weight rows and all tokens; its
+// waves split K by chunks of 64 bytes of a row, all loads linear, and meet in LDS
+// in a fixed order.
+constexpr int kRowWaves = 8;
+
+template <typename T, int BITS, int TB>
+__global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, const half8* __restrict__ hi,
+                                                                 const half8* __restrict__ lo,
+                                                                 const float* __restrict__ inv, int calls, bool whole) {
+    using M = MfmaCodec<BITS>;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int n = lane & 15, g = lane >> 4;
-    const int tiles = (a.N + 15) / 16, r0 = blockIdx.x % tiles * 16, t0 = blockIdx.x / tiles * 16;
-    const int groups = a.K / CW, chunks = (groups + 3) / 4;
+    const int r0 = blockIdx.x * 16, last_tb = (int)blocks16(a.T) - 1;
+    const int groups = a.K / (128 / BITS), chunks = (groups + 3) / 4;
     const uint8_t* wrow = a.w + (int64_t)min(r0 + n, a.N - 1) * groups * 16;
-    const int64_t xrow = (int64_t)min(t0 + n, a.T - 1) * Kp;
-    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int ch = wave; ch < chunks; ch += kWaves) {
-        const int gr = ch * 4 + g;
-        uint4 q = {0, 0, 0, 0};
-        if (gr < groups) q = ld16(wrow + (int64_t)gr * 16);
+    Params par;
+    if (wave < TB) par = load_params(a, r0 + 4 * g);
+    floatx4 acc[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int ch = wave; ch < chunks; ch += kRowWaves) {
+        const uint4 q = ld16(wrow + (int64_t)min(4 * ch + g, groups - 1) * 16);
 #pragma unroll
         for (int c = 0; c < M::NCALL; ++c) {
             const half8 w = a_operand<BITS>(q, c);
-            acc = mfma::mfma(w, *reinterpret_cast<const half8*>(hi + xrow + (int64_t)gr * CW + 8 * c), acc);
-            if (T::bytes == 4)
-                acc = mfma::mfma(w, *reinterpret_cast<const half8*>(lo + xrow + (int64_t)gr * CW + 8 * c), acc);
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const int64_t at = ((int64_t)min(t, last_tb) * calls + ch * M::NCALL + c) * kWave + lane;
+                acc[t] = mfma::mfma(w, hi[at], acc[t]);
+                if (T::bytes == 4) acc[t] = mfma::mfma(w, lo[at], acc[t]);
+            }
         }
     }
-    __shared__ floatx4 part[kWaves][kWave];
+    __shared__ floatx4 part[kRowWaves][TB][kWave];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) part[wave][t][lane] = acc[t];
+    __syncthreads();
+    for (int t = wave; t < TB; t += kRowWaves) {
+        floatx4 v = part[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < kRowWaves; ++w) v += part[w][t][lane];
+        const int tok = t * 16 + n;
+        if (tok < a.T) finish4<T>(a, tok, r0 + 4 * g, inv[tok], v, par, whole);
+    }
+}
+
+// -------------------------------------------------------------- few tokens
+//
+// Up to kFewTokens tokens whose fp16 form fits in LDS, in one launch: every
+// workgroup converts the activations itself while its first weight loads are in
+// flight.  With one to eight tokens the 16 MFMA columns hold the hi parts (0 ..
+// 7) and, for fp32, the lo parts (8 .. 15) side by side, so a pair costs no
+// second MFMA; columns without a token repeat one and are dropped.
+constexpr int kFewTokens = 8;
+constexpr int kFewLds = 64 * 1024;
+constexpr int kFewFlight = 8;             // chunks a wave has in flight
+constexpr int kFewUnits = 8;              // units a thread converts at most
+
+template <typename T, int BITS>
+__global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, int calls, bool whole) {
+    using M = MfmaCodec<BITS>;
+    constexpr int CW = 128 / BITS;
+    constexpr int kThreads = kRowWaves * kWave;
+    constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
+    extern __shared__ half8 xs[];                          // [token][plane][call][lane group]
+    __shared__ unsigned top[kFewTokens];                   // largest magnitudes as bits (they are not negative)
+    __shared__ floatx4 part[kRowWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int n = lane & 15, g = lane >> 4;
+    const int r0 = blockIdx.x * 16, units = calls * 4, total = a.T * units;
+    const int groups = a.K / CW, chunks = (groups + 3) / 4;
+    const uint8_t* wrow = a.w + (int64_t)min(r0 + n, a.N - 1) * groups * 16;
+    if (threadIdx.x < kFewTokens) top[threadIdx.x] = 0;
+
+    // the activations first: what waits for them need not wait for the weights
+    const typename T::type* x = reinterpret_cast<const typename T::type*>(a.x);
+    float v[kFewUnits][8];
+#pragma unroll
+    for (int i = 0; i < kFewUnits; ++i) {
+        const int k = threadIdx.x + i * kThreads;
+        if (i * kThreads < total) {
+            const int t = min(k, total - 1) / units;
+            load_unit<T, BITS>(x + t * a.ldx, k < total ? a.K : 0, k - t * units, v[i]);
+        }
+    }
+    uint4 q[kFewFlight];
+#pragma unroll
+    for (int i = 0; i < kFewFlight; ++i)
+        if (i == 0 || i * kRowWaves < chunks)
+            q[i] = ld16(wrow + (int64_t)min(4 * (wave + i * kRowWaves) + g, groups - 1) * 16);
+    Params par;
+    if (wave == 0) par = load_params(a, r0 + 4 * g);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFewUnits; ++i) {
+        const int k = threadIdx.x + i * kThreads;
+        if (i * kThreads < total) {
+            // 16 consecutive units belong to one token (units is a multiple of 16)
+            float m = max8(v[i], 0.f);
+            m = fmaxf(m, dpp_f<0xB1>(m));
+            m = fmaxf(m, dpp_f<0x4E>(m));
+            m = fmaxf(m, dpp_f<0x141>(m));
+            m = fmaxf(m, dpp_f<0x140>(m));
+            if ((lane & 15) == 0 && k < total) atomicMax(&top[k / units], __float_as_uint(m));
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFewUnits; ++i) {
+        const int k = threadIdx.x + i * kThreads;
+        if (k < total) {
+            const int t = k / units;
+            half8 h, l;
+            split_unit<BITS>(v[i], pow2(row_exponent(__uint_as_float(top[t]))), h, l);
+            xs[kPlanes * t * units + k - t * units] = h;
+            if (kPlanes == 2) xs[(2 * t + 1) * units + k - t * units] = l;
+        }
+    }
+    __syncthreads();
+
+    const int tok = kPlanes == 2 ? n & 7 : n;
+    const half8* mine = xs + (kPlanes * min(tok, a.T - 1) + (kPlanes == 2 ? n >> 3 : 0)) * units + g;
+    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = wave; c0 < chunks; c0 += kFewFlight * kRowWaves) {
+#pragma unroll
+        for (int i = 0; i < kFewFlight; ++i) {
+            const int ch = c0 + i * kRowWaves;
+            if (ch < chunks) {
+#pragma unroll
+                for (int c = 0; c < M::NCALL; ++c)
+                    acc = mfma::mfma(a_operand<BITS>(q[i], c), mine[(ch * M::NCALL + c) * 4], acc);
+            }
+            const int nx = ch + kFewFlight * kRowWaves;
+            if (nx < chunks) q[i] = ld16(wrow + (int64_t)min(4 * nx + g, groups - 1) * 16);
+        }
+    }
     part[wave][lane] = acc;
     __syncthreads();
     if (wave != 0) return;
-    const int t = t0 + n;
-    if (t >= a.T) return;
-    typename T::type* y = reinterpret_cast<typename T::type*>(a.y) + (int64_t)t * a.ldy;
-    const typename T::type* res = reinterpret_cast<const typename T::type*>(a.residual) + (int64_t)t * a.ldr;
+    floatx4 sum = part[0][lane];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * g + i;
-        if (r >= a.N) break;
-        float v = (part[0][lane][i] + part[1][lane][i]) + (part[2][lane][i] + part[3][lane][i]);
-        v = v * inv[t] * a.scale[r];
-        if (a.bias) v += a.bias[r];
-        v = activate(v, a.act);
-        if (a.residual) v += T::get(res[r]);
-        y[r] = T::put(v);
+    for (int w = 1; w < kRowWaves; ++w) sum += part[w][lane];
+    if (kPlanes == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor(sum[i], 8, kWave);
     }
+    if (tok >= a.T || (kPlanes == 2 && n >= 8)) return;
+    finish4<T>(a, tok, r0 + 4 * g, pow2(-row_exponent(__uint_as_float(top[tok]))), sum, par, whole);
+}
+
+// ------------------------------------------------------------------- launches
+
+constexpr int kRowsTokens = 64;           // linear_rows up to here
+
+bool few(const LinearArgs& a, int bits, int bytes) {
+    const int64_t n = a.T * padded(a.K, bits);
+    return a.T <= kFewTokens && n * (bytes == 4 ? 4 : 2) <= kFewLds && n / 8 <= kFewUnits * kRowWaves * kWave;
+}
+
+// One store of four outputs is possible.
+bool whole4(const LinearArgs& a, int bytes) {
+    const uintptr_t m = 4 * bytes - 1;
+    return !(reinterpret_cast<uintptr_t>(a.y) & m) && !(a.ldy * bytes & m);
+}
+
+template <typename T, int BITS, int NB, int TB, int WN, int WT>
+void launch_gemm(const LinearArgs& a, const half8* hi, const half8* lo, const float* inv, int calls, hipStream_t st) {
+    const int64_t tiles = (int64_t)((a.N + WN * NB * 16 - 1) / (WN * NB * 16)) *
+                          ((a.T + WT * TB * 16 - 1) / (WT * TB * 16));
+    hipLaunchKernelGGL((linear_gemm<T, BITS, NB, TB, WN, WT>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                       dim3(WN * WT * kWave), 0, st, a, hi, lo, inv, calls, whole4(a, T::bytes));
+}
+
+template <typename T, int BITS, int NU>
+void launch_prepare(const LinearArgs& a, half8* hi, half8* lo, float* inv, int calls, hipStream_t st) {
+    const int64_t grid = (blocks16(a.T) + 7) / 8 * 8 * (16 / (kPrepThreads / kWave));
+    hipLaunchKernelGGL((linear_prepare<T, BITS, NU>), dim3((unsigned)grid), dim3(kPrepThreads), 0, st,
+                       reinterpret_cast<const typename T::type*>(a.x), a.ldx, a.T, a.K, calls, hi, lo, inv);
 }
 
 template <typename T, int BITS>
 hipError_t launch_bits(const LinearArgs& a, hipStream_t st) {
-    const int64_t Kp = padded(a.K);
-    _Float16* hi = reinterpret_cast<_Float16*>(a.workspace);
-    _Float16* lo = hi + (T::bytes == 4 ? (int64_t)a.T * Kp : 0);
-    float* inv = reinterpret_cast<float*>(lo + (int64_t)a.T * Kp);
-    hipLaunchKernelGGL((linear_prepare<T, BITS>), dim3(a.T), dim3(kPrepThreads), 0, st,
-                       reinterpret_cast<const typename T::type*>(a.x), a.ldx, a.K, (int)Kp, hi, lo, inv);
-    hipLaunchKernelGGL((linear_simple<T, BITS>), dim3((unsigned)linear_grid(a)), dim3(kThreads), 0, st, a,
-                       (int)Kp, hi, lo, inv);
+    const int64_t Kp = padded(a.K, BITS);
+    const int calls = (int)(Kp / 32);
+    const bool whole = whole4(a, T::bytes);
+    const dim3 rows((a.N + 15) / 16), rt(kRowWaves * kWave);
+    if (few(a, BITS, T::bytes)) {
+        const size_t lds = (size_t)a.T * Kp * (T::bytes == 4 ? 4 : 2);
+        hipLaunchKernelGGL((linear_few<T, BITS>), rows, rt, lds, st, a, calls, whole);
+        return hipGetLastError();
+    }
+    const int64_t blocks = blocks16(a.T);
+    half8* hi = reinterpret_cast<half8*>(a.workspace);
+    half8* lo = hi + (T::bytes == 4 ? blocks * calls * kWave : 0);
+    float* inv = reinterpret_cast<float*>(lo + blocks * calls * kWave);
+    if (calls <= 64) launch_prepare<T, BITS, 4>(a, hi, lo, inv, calls, st);
+    else if (calls <= 128) launch_prepare<T, BITS, 8>(a, hi, lo, inv, calls, st);
+    else if (calls <= 256) launch_prepare<T, BITS, 16>(a, hi, lo, inv, calls, st);
+    else launch_prepare<T, BITS, 0>(a, hi, lo, inv, calls, st);
+    if (a.T <= 16) hipLaunchKernelGGL((linear_rows<T, BITS, 1>), rows, rt, 0, st, a, hi, lo, inv, calls, whole);
+    else if (a.T <= 32) hipLaunchKernelGGL((linear_rows<T, BITS, 2>), rows, rt, 0, st, a, hi, lo, inv, calls, whole);
+    else if (a.T <= 48) hipLaunchKernelGGL((linear_rows<T, BITS, 3>), rows, rt, 0, st, a, hi, lo, inv, calls, whole);
+    else if (a.T <= kRowsTokens)
+        hipLaunchKernelGGL((linear_rows<T, BITS, 4>), rows, rt, 0, st, a, hi, lo, inv, calls, whole);
+    else {
+        // the largest tile that still gives most compute units a workgroup
+        const int64_t big = (int64_t)((a.N + 255) / 256) * ((a.T + 255) / 256);
+        const int64_t mid = (int64_t)((a.N + 127) / 128) * ((a.T + 127) / 128);
+        if (big >= 200) launch_gemm<T, BITS, 4, 8, 4, 2>(a, hi, lo, inv, calls, st);
+        else if (mid >= 200) launch_gemm<T, BITS, 4, 4, 2, 2>(a, hi, lo, inv, calls, st);
+        else launch_gemm<T, BITS, 2, 2, 2, 2>(a, hi, lo, inv, calls, st);
+    }
     return hipGetLastError();
 }
 
@@ -157,10 +592,10 @@ hipError_t launch_type(int bits, const LinearArgs& a, hipStream_t st) {
 
 int64_t linear_workspace(int dtype, int64_t T, int64_t K) {
     if (T == 0) return 0;
-    return T * padded(K) * (dtype == MOEDEC_F32 ? 4 : 2) + (T * 4 + 15) / 16 * 16;
+    return blocks16(T) * 16 * (padded(K, 2) * (dtype == MOEDEC_F32 ? 4 : 2) + 4);
 }
 
-int64_t linear_grid(const LinearArgs& a) { return (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16); }
+int64_t linear_grid(const LinearArgs& a) { return (int64_t)((a.N + 63) / 64) * ((a.T + 63) / 64) + 8; }
 
 hipError_t launch_linear(int bits, int dtype, const LinearArgs& a, hipStream_t st) {
     if (a.T == 0) return hipSuccess;
