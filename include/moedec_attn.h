@@ -49,7 +49,7 @@ extern "C" {
  *   residual : [T] rows of N elements of `dtype`, ldr apart, or NULL; may be y
  *              itself (with ldr == ldy)
  *   y        : [T] rows of N elements of `dtype`, ldy apart; must not overlap x
- *   workspace: dense_linear_workspace(dtype, T, K) bytes of device memory,
+ *   workspace: dense_linear_workspace(...) bytes of device memory,
  *              16-byte aligned (NULL when that is 0); calls that may run at
  *              the same time need separate ones
  * Products with fp16 and bf16 activations are exact (every activation of a row
@@ -57,12 +57,13 @@ extern "C" {
  * 2^-29 of the row's largest lose bits), fp32 activations enter with about 22
  * bits; sums are fp32; y is rounded once.  A row of x that holds a NaN or an
  * infinity gives unspecified values in that row of y only.
- * T == 0 is a no-op.  Requires K a positive multiple of 128/bits, N >= 1,
+ * T == 0 is a no-op.  dense_linear_workspace gives -1 for sizes that are refused.
+ * Requires K a positive multiple of 128/bits, N >= 1,
  * x and w 16-byte aligned, ldx*element size a multiple of 16, ldx >= K,
- * ldr, ldy >= N (INVALID_ARG); K <= 65536, T and N < 2^24 and T*N/256 < 2^31
+ * ldr, ldy >= N (INVALID_ARG); K <= 65536, T and N < 2^24 and T*N/512 < 2^31
  * (UNSUPPORTED).
  */
-int64_t dense_linear_workspace(int dtype, int64_t T, int64_t K);
+int64_t dense_linear_workspace(int bits, int dtype, int64_t T, int64_t K, int64_t N);
 int dense_linear_q4(const void* x, int dtype, int64_t ldx, const uint8_t* w, const float* scale, const float* bias,
                     int act, const void* residual, int64_t ldr, void* y, int64_t ldy, int64_t T, int64_t K, int64_t N,
                     void* workspace, int64_t workspace_bytes, void* stream);

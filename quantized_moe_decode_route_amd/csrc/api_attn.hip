@@ -84,7 +84,7 @@ int linear(int bits, const void* x, int dtype, int64_t ldx, const uint8_t* w, co
     if ((reinterpret_cast<uintptr_t>(y) & e) || (reinterpret_cast<uintptr_t>(residual) & e))
         return MOEDEC_ERR_INVALID_ARG;
     if (K > 65536 || T >= kMaxRows || N >= kMaxRows) return MOEDEC_ERR_UNSUPPORTED;
-    const int64_t need = linear_workspace(dtype, T, K);
+    const int64_t need = linear_workspace(bits, dtype, T, K, N);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return MOEDEC_ERR_INVALID_ARG;
     LinearArgs a;
     a.x = x;
@@ -107,9 +107,11 @@ int linear(int bits, const void* x, int dtype, int64_t ldx, const uint8_t* w, co
 
 }  // namespace
 
-MOEDEC_API int64_t dense_linear_workspace(int dtype, int64_t T, int64_t K) {
-    if (!dtype_ok(dtype) || T < 0 || K < 1 || K > 65536 || T >= kMaxRows) return -1;
-    return linear_workspace(dtype, T, K);
+MOEDEC_API int64_t dense_linear_workspace(int bits, int dtype, int64_t T, int64_t K, int64_t N) {
+    if ((bits != 4 && bits != 8 && bits != 2) || !dtype_ok(dtype) || T < 0 || K < 1 || N < 1 || K > 65536 ||
+        T >= kMaxRows || N >= kMaxRows)
+        return -1;
+    return linear_workspace(bits, dtype, T, K, N);
 }
 
 #define DENSE_LINEAR(BITS)                                                                                            \

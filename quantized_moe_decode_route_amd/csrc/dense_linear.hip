@@ -20,8 +20,13 @@ namespace attn {
 
 namespace {
 
-using mfma::a_operand;
 using mfma::MfmaCodec;
+
+template <int BITS>
+__device__ __forceinline__ half8 a_operand(const uint4& q, int c) {
+    if constexpr (BITS == 4) return codes_f16(mfma::dword(q, c));
+    else return mfma::a_operand<BITS>(q, c);
+}
 
 constexpr int kPrepThreads = 256;
 constexpr int kStage = 4;                 // MFMA calls (of 32 columns) of a staged step
@@ -167,20 +172,23 @@ __device__ __forceinline__ float max8(const float* v, float m) {
 // load of it is linear.  Call q of chunk c multiplies the columns that a_operand
 // gives for call q of a 16-byte group of codes.
 //
-// One wave a token.  Rows of up to 512 * NU columns stay in registers between the
-// pass for the largest magnitude and the conversion (NU = 0: read twice).
-// HBM-bound: x read once, the planes written once; the 16 bytes a lane stores
-// meet those of the block's other tokens in the L2 of one XCD.
-template <typename T, int BITS, int NU>
+// WPT waves a token.  Rows of up to 512 * WPT * NU columns stay in registers
+// between the pass for the largest magnitude and the conversion (NU = 0: read
+// twice).  HBM-bound for many tokens (x read once, the planes written once; the 16
+// bytes a lane stores meet those of the block's other tokens in the L2 of one
+// XCD), a few microseconds of latency for few: those take four waves a token.
+template <typename T, int BITS, int NU, int WPT>
 __global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T::type* __restrict__ x, int64_t ldx,
                                                                int T_, int K, int calls, half8* __restrict__ hi,
                                                                half8* __restrict__ lo, float* __restrict__ inv) {
-    const int lane = threadIdx.x & (kWave - 1);
-    // the waves of a block of 16 tokens run on one XCD (workgroups go to the XCDs round robin)
-    constexpr int kParts = 16 / (kPrepThreads / kWave);
+    constexpr int kPer = kPrepThreads / kWave / WPT;       // tokens of a workgroup
+    constexpr int kParts = 16 / kPer;                      // workgroups of a block of 16 tokens: all on one XCD
+    constexpr int kLanes = WPT * kWave;
+    __shared__ float red[kPrepThreads / kWave];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), j = threadIdx.x % kLanes;
     const int xcd = blockIdx.x % 8, i8 = blockIdx.x / 8;
     const int64_t block = (int64_t)(i8 / kParts) * 8 + xcd;
-    const int n = i8 % kParts * (kPrepThreads / kWave) + threadIdx.x / kWave;
+    const int n = i8 % kParts * kPer + wave / WPT;
     const int64_t t = block * 16 + n;
     if (block * 16 >= T_) return;
     const bool on = t < T_;
@@ -193,32 +201,39 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T:
         hi[at] = h;
         if (T::bytes == 4) lo[at] = l;
     };
+    auto row_max = [&](float m) {
+        m = wave_max(m);
+        if constexpr (WPT == 1) return m;
+        if ((threadIdx.x & (kWave - 1)) == 0) red[wave] = m;
+        __syncthreads();
+        return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    };
     float m = 0.f;
     if constexpr (NU > 0) {
         float v[NU][8];
 #pragma unroll
-        for (int i = 0; i < NU; ++i) load_unit<T, BITS>(row, lane + i * kWave < units ? cols : 0, lane + i * kWave, v[i]);
+        for (int i = 0; i < NU; ++i) load_unit<T, BITS>(row, j + i * kLanes < units ? cols : 0, j + i * kLanes, v[i]);
 #pragma unroll
         for (int i = 0; i < NU; ++i) m = max8(v[i], m);
-        m = wave_max(m);
+        m = row_max(m);
         const float f = pow2(row_exponent(m));
 #pragma unroll
         for (int i = 0; i < NU; ++i)
-            if (lane + i * kWave < units) put(lane + i * kWave, v[i], f);
+            if (j + i * kLanes < units) put(j + i * kLanes, v[i], f);
     } else {
         float v[8];
-        for (int u = lane; u < units; u += kWave) {
+        for (int u = j; u < units; u += kLanes) {
             load_unit<T, BITS>(row, cols, u, v);
             m = max8(v, m);
         }
-        m = wave_max(m);
+        m = row_max(m);
         const float f = pow2(row_exponent(m));
-        for (int u = lane; u < units; u += kWave) {
+        for (int u = j; u < units; u += kLanes) {
             load_unit<T, BITS>(row, cols, u, v);
             put(u, v, f);
         }
     }
-    if (lane == 0) inv[t] = pow2(-row_exponent(m));
+    if (j == 0) inv[t] = pow2(-row_exponent(m));
 }
 
 // ------------------------------------------------------------- many tokens
@@ -259,35 +274,47 @@ __device__ __forceinline__ half8 step_operand(const Packed<BITS>& p, int c) {
     else return a_operand<2>(uint4{p.w[0], p.w[1], 0, 0}, c);
 }
 
-// Workgroup tile: WN * NB * 16 weight rows by WT * TB * 16 tokens, WN x WT waves.
-// Per step of 128 columns the activations (WT * TB * 4 KB) go to one of two LDS
-// buffers by direct loads while the other is multiplied; each wave keeps the next
-// step's packed codes in registers.  One barrier a step.  fp32: a step is 64
-// columns of both planes, each converted code used twice.
+// Workgroup tile: WN * NB * 16 weight rows by WT * TB * 16 tokens, WN x WT waves,
+// over the steps of one of `splits` equal parts of K.  A step is 128 columns (fp32:
+// 64 columns of both planes, each converted code used twice).  The activations of
+// a step (WT * TB * 4 KB) go to one of D LDS buffers by direct loads, the packed
+// codes to registers, D - 1 steps ahead; one barrier a step.  With one part the
+// tile is finished here, else its fp32 sums go to `part` [split][token][row].
 //
-// Bound by the matrix cores: a wave's step is 4 * NB * TB MFMAs of 16 cycles
-// against 4 * NB conversions of 9 vector instructions.  Workgroups are dealt to
-// the eight XCDs in contiguous runs of tiles, four token tiles by the weight
-// tiles, so that an XCD's L2 serves each activation tile to several workgroups.
-template <typename T, int BITS, int NB, int TB, int WN, int WT>
+// Bound by the matrix cores where tokens are many: a wave's step is 4 * NB * TB
+// MFMAs of 16 cycles against 4 * NB conversions of 9 vector instructions.
+// Workgroups are dealt to the eight XCDs in contiguous runs of tiles, four token
+// tiles by the weight tiles, so that an XCD's L2 serves each activation tile to
+// several workgroups.
+template <int N>
+__device__ __forceinline__ void wait_loads_and_barrier() {
+    // all but the last N loads of this wave have landed; then the workgroup meets
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <typename T, int BITS, int NB, int TB, int WN, int WT, int D>
 __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, const half8* __restrict__ hi,
                                                                const half8* __restrict__ lo,
-                                                               const float* __restrict__ inv, int calls, bool whole) {
+                                                               const float* __restrict__ inv, float* __restrict__ part,
+                                                               int calls, int splits, bool whole) {
     constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
     constexpr int kW = WN * WT;
     constexpr int kLoads = WT * TB * kStage / kW;          // 1 KB direct loads a wave makes per step
     static_assert(WT * TB * kStage % kW == 0, "direct loads divide over the waves");
-    __shared__ half8 buf[2][WT * TB * kStage * kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    __shared__ half8 buf[D][WT * TB * kStage * kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4, wn = wave % WN, wt = wave / WN;
     const int tiles_n = (a.N + WN * NB * 16 - 1) / (WN * NB * 16), tiles_t = (a.T + WT * TB * 16 - 1) / (WT * TB * 16);
-    const int total = tiles_n * tiles_t, per = (total + 7) / 8;
-    const int id = blockIdx.x % 8 * per + blockIdx.x / 8;
-    if (blockIdx.x / 8 >= per || id >= total) return;
+    const int total = tiles_n * tiles_t * splits, per = (total + 7) / 8;
+    const int unit = blockIdx.x % 8 * per + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= per || unit >= total) return;
+    const int id = unit / splits, split = unit % splits;
     const int band = id / (4 * tiles_n), in = id % (4 * tiles_n), high = min(tiles_t - 4 * band, 4);
     const int tile_t = 4 * band + in % high, tile_n = in / high;
     const int r0 = (tile_n * WN + wn) * NB * 16, tb0 = tile_t * WT * TB, last_tb = (int)blocks16(a.T) - 1;
-    const int groups = a.K / (128 / BITS), steps = calls / kStage;
+    const int groups = a.K / (128 / BITS);
+    const int packs = calls / kStage, p0 = (int)((int64_t)packs * split / splits),
+              p1 = (int)((int64_t)packs * (split + 1) / splits), steps = (p1 - p0) * kPlanes;
     // the tile's rows by 32-bit offsets (at most 256 rows of 64 KB)
     const int tr0 = tile_n * WN * NB * 16;
     const uint8_t* wtile = a.w + (int64_t)tr0 * groups * 16;
@@ -296,7 +323,7 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
     for (int b = 0; b < NB; ++b) wrow[b] = (uint32_t)(min(r0 + 16 * b + n, a.N - 1) - tr0) * (uint32_t)(groups * 16);
 
     // LDS unit k (0 .. 3) of a token block: call k, or (fp32) plane k / 2 of call k % 2
-    auto stage = [&](int s, int to) {
+    auto stage = [&](int s, half8* to) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int u = wave * kLoads + i;                               // (token block, call)
@@ -304,7 +331,7 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
             const int k = u % kStage;
             const half8* src = (kPlanes == 2 && k >= 2 ? lo : hi) +
                                ((int64_t)tb * calls + (kPlanes == 2 ? 2 * s + (k & 1) : kStage * s + k)) * kWave + lane;
-            __builtin_amdgcn_global_load_lds((gptr_t)src, (lptr_t)&buf[to][u * kWave], 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((gptr_t)src, (lptr_t)(to + u * kWave), 16, 0, 0);
         }
     };
 
@@ -313,30 +340,54 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int t = 0; t < TB; ++t) acc[b][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-    Packed<BITS> next[NB], cur[NB];
+    // Packed steps held.  One plane: the ring follows the buffers (with one step
+    // ahead the loop is not unrolled and the next codes move over: unrolled by two
+    // it spilled registers).  Two planes: a packed step lasts two steps, the next
+    // one is loaded at the first of them into the other slot.
+    constexpr bool kMove = D == 2 && kPlanes == 1;
+    constexpr int kUnroll = kMove ? 1 : 4;
+    constexpr int kPackRing = kMove || kPlanes == 2 ? 2 : D;
+    static_assert(kMove || D == 4 || (D == 2 && kPlanes == 2), "static buffer turns");
+    Packed<BITS> pk[kPackRing][NB];
+    auto codes = [&](Packed<BITS>* to, int p) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) next[b] = load_packed<BITS>(wtile, wrow[b], groups, 0, g);
-    stage(0, 0);
-    for (int p = 0; p < steps; ++p) {                      // 128 columns: one packed step
+        for (int b = 0; b < NB; ++b) to[b] = load_packed<BITS>(wtile, wrow[b], groups, p0 + p, g);
+    };
+    const int first = p0 * kPlanes;
+    if (kMove) codes(pk[1], 0);
+    if (kPlanes == 2) codes(pk[0], 0);
 #pragma unroll
-        for (int h = 0; h < kPlanes; ++h) {
-            const int s = p * kPlanes + h;
-            __syncthreads();                               // step s is in LDS, step s - 1 is done with
-            if (h == 0) {
+    for (int j = 0; j < D - 1; ++j) {
+        if (j >= steps) break;
+        if (kPlanes == 1 && !kMove) codes(pk[j % kPackRing], j);
+        stage(first + j, buf[j]);
+    }
+    for (int s0 = 0; s0 < steps; s0 += kUnroll) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b) cur[b] = next[b];
+        for (int j = 0; j < kUnroll; ++j) {
+            const int s = s0 + j;
+            if (s >= steps) break;
+            // step s has landed once only the loads of the steps after it are left: at least
+            // (D - 2) * kLoads direct loads (fewer steps remain at the end: then all)
+            if (D > 2 && s + D - 1 <= steps) wait_loads_and_barrier<(D > 2 ? (D - 2) * kLoads : 0)>();
+            else wait_loads_and_barrier<0>();
+            const int nx = s + D - 1;
+            if (kMove) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) pk[0][b] = pk[1][b];
             }
-            if (s + 1 < steps * kPlanes) stage(s + 1, (s + 1) & 1);
-            if (h == 0 && p + 1 < steps) {
-#pragma unroll
-                for (int b = 0; b < NB; ++b) next[b] = load_packed<BITS>(wtile, wrow[b], groups, p + 1, g);
+            if (kPlanes == 2 && j % 2 == 0 && s + 2 < steps) codes(pk[(j / 2 + 1) % 2], s / 2 + 1);
+            if (nx < steps) {
+                if (kPlanes == 1) codes(pk[kMove ? 1 : (j + D - 1) % kPackRing], nx);
+                stage(first + nx, buf[kMove ? nx & 1 : (j + D - 1) % D]);
             }
-            const half8* x = buf[s & 1] + wt * TB * kStage * kWave + lane;
+            const half8* x = buf[kMove ? s & 1 : j % D] + wt * TB * kStage * kWave + lane;
 #pragma unroll
             for (int c = 0; c < kStage / kPlanes; ++c) {
                 half8 w[NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) w[b] = step_operand<BITS>(cur[b], kPlanes == 2 ? 2 * h + c : c);
+                for (int b = 0; b < NB; ++b)
+                    w[b] = step_operand<BITS>(pk[kMove ? 0 : kPlanes == 2 ? j / 2 : j % kPackRing][b], kPlanes == 2 ? 2 * (j % 2) + c : c);
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -351,6 +402,16 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int r = r0 + 16 * b + 4 * g;
+        if (splits > 1) {
+            if (r >= a.N) continue;
+            const int64_t ldp = (a.N + 3) / 4 * 4;
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const int tok = (tb0 + wt * TB + t) * 16 + n;
+                if (tok < a.T) *reinterpret_cast<floatx4*>(part + ((int64_t)split * a.T + tok) * ldp + r) = acc[b][t];
+            }
+            continue;
+        }
         const Params par = load_params(a, r);
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
@@ -360,53 +421,109 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
     }
 }
 
+// The sum of the parts of K in their order, and the epilogue: four rows a thread.
+constexpr int kJoinThreads = 256;
+template <typename T>
+__global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const float* __restrict__ inv,
+                                                            const float* __restrict__ part, int splits, bool whole) {
+    const int quads = (a.N + 3) / 4, blocks = (quads + kJoinThreads - 1) / kJoinThreads;
+    const int t = blockIdx.x / blocks, r = (blockIdx.x % blocks * kJoinThreads + threadIdx.x) * 4;
+    if (r >= a.N) return;
+    const Params par = load_params(a, r);
+    const floatx4* p = reinterpret_cast<const floatx4*>(part) + (int64_t)t * quads + r / 4;
+    floatx4 v = p[0];
+#pragma unroll 4
+    for (int s = 1; s < splits; ++s) v += p[(int64_t)s * a.T * quads];
+    finish4<T>(a, t, r, inv[t], v, par, whole);
+}
+
 // ------------------------------------------------------------- some tokens
 //
-// Up to TB * 16 tokens: bound by the weights' bytes (and, from some 30 tokens on,
-// by the planes' L2 reads).  A workgroup owns 16 weight rows and all tokens; its
-// waves split K by chunks of 64 bytes of a row, all loads linear, and meet in LDS
-// in a fixed order.
+// Up to TB * 16 tokens: bound by the weights' bytes and the planes' L2 reads.  A
+// workgroup owns NB * 16 weight rows and all tokens; its waves split K by chunks
+// of 64 bytes of a row, all loads linear, kRowFlight chunks of codes in flight,
+// and meet in LDS in a fixed order.
 constexpr int kRowWaves = 8;
+constexpr int kRowFlight = 4;               // even: the operands' two buffers alternate with it
 
-template <typename T, int BITS, int TB>
+template <typename T, int BITS, int TB, int NB>
 __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, const half8* __restrict__ hi,
                                                                  const half8* __restrict__ lo,
                                                                  const float* __restrict__ inv, int calls, bool whole) {
     using M = MfmaCodec<BITS>;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
-    const int r0 = blockIdx.x * 16, last_tb = (int)blocks16(a.T) - 1;
+    const int r0 = blockIdx.x * 16 * NB, last_tb = (int)blocks16(a.T) - 1;
     const int groups = a.K / (128 / BITS), chunks = (groups + 3) / 4;
-    const uint8_t* wrow = a.w + (int64_t)min(r0 + n, a.N - 1) * groups * 16;
+    const uint8_t* wrow[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) wrow[b] = a.w + (int64_t)min(r0 + 16 * b + n, a.N - 1) * groups * 16;
+    auto codes = [&](int b, int ch) { return ld16(wrow[b] + (int64_t)min(4 * ch + g, groups - 1) * 16); };
+    uint4 q[kRowFlight][NB];
+#pragma unroll
+    for (int i = 0; i < kRowFlight; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) q[i][b] = codes(b, wave + i * kRowWaves);
+    constexpr int kFinish = TB * NB;                       // 16 x 16 blocks to finish, one a wave
+    const int ft = wave % TB, fb = wave / TB % NB;
     Params par;
-    if (wave < TB) par = load_params(a, r0 + 4 * g);
-    floatx4 acc[TB];
+    if (wave < kFinish) par = load_params(a, r0 + 16 * fb + 4 * g);
+    floatx4 acc[TB][NB];
 #pragma unroll
-    for (int t = 0; t < TB; ++t) acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int ch = wave; ch < chunks; ch += kRowWaves) {
-        const uint4 q = ld16(wrow + (int64_t)min(4 * ch + g, groups - 1) * 16);
+    for (int t = 0; t < TB; ++t)
 #pragma unroll
-        for (int c = 0; c < M::NCALL; ++c) {
-            const half8 w = a_operand<BITS>(q, c);
+        for (int b = 0; b < NB; ++b) acc[t][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+    // the planes' operands of a chunk, one chunk ahead
+    constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
+    half8 xv[2][M::NCALL][TB][kPlanes];
+    auto acts = [&](half8 (*to)[TB][kPlanes], int ch) {
+#pragma unroll
+        for (int c = 0; c < M::NCALL; ++c)
 #pragma unroll
             for (int t = 0; t < TB; ++t) {
                 const int64_t at = ((int64_t)min(t, last_tb) * calls + ch * M::NCALL + c) * kWave + lane;
-                acc[t] = mfma::mfma(w, hi[at], acc[t]);
-                if (T::bytes == 4) acc[t] = mfma::mfma(w, lo[at], acc[t]);
+                to[c][t][0] = hi[at];
+                if (kPlanes == 2) to[c][t][kPlanes - 1] = lo[at];
+            }
+    };
+    if (wave < chunks) acts(xv[0], wave);
+    for (int c0 = wave; c0 < chunks; c0 += kRowFlight * kRowWaves) {
+#pragma unroll
+        for (int i = 0; i < kRowFlight; ++i) {
+            const int ch = c0 + i * kRowWaves;
+            if (ch >= chunks) break;
+            if (ch + kRowWaves < chunks) acts(xv[(i + 1) & 1], ch + kRowWaves);
+#pragma unroll
+            for (int c = 0; c < M::NCALL; ++c) {
+                half8 w[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) w[b] = a_operand<BITS>(q[i][b], c);
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+#pragma unroll
+                    for (int k = 0; k < kPlanes; ++k)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) acc[t][b] = mfma::mfma(w[b], xv[i & 1][c][t][k], acc[t][b]);
+            }
+            const int nx = ch + kRowFlight * kRowWaves;
+            if (nx < chunks) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) q[i][b] = codes(b, nx);
             }
         }
     }
-    __shared__ floatx4 part[kRowWaves][TB][kWave];
+    __shared__ floatx4 part[kRowWaves][kFinish][kWave];
 #pragma unroll
-    for (int t = 0; t < TB; ++t) part[wave][t][lane] = acc[t];
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) part[wave][b * TB + t][lane] = acc[t][b];
     __syncthreads();
-    for (int t = wave; t < TB; t += kRowWaves) {
-        floatx4 v = part[0][t][lane];
+    if (wave >= kFinish) return;
+    floatx4 v = part[0][wave][lane];
 #pragma unroll
-        for (int w = 1; w < kRowWaves; ++w) v += part[w][t][lane];
-        const int tok = t * 16 + n;
-        if (tok < a.T) finish4<T>(a, tok, r0 + 4 * g, inv[tok], v, par, whole);
-    }
+    for (int w = 1; w < kRowWaves; ++w) v += part[w][wave][lane];
+    const int tok = ft * 16 + n;
+    if (tok < a.T) finish4<T>(a, tok, r0 + 16 * fb + 4 * g, inv[tok], v, par, whole);
 }
 
 // -------------------------------------------------------------- few tokens
@@ -430,7 +547,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
     extern __shared__ half8 xs[];                          // [token][plane][call][lane group]
     __shared__ unsigned top[kFewTokens];                   // largest magnitudes as bits (they are not negative)
     __shared__ floatx4 part[kRowWaves][kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
     const int r0 = blockIdx.x * 16, units = calls * 4, total = a.T * units;
     const int groups = a.K / CW, chunks = (groups + 3) / 4;
@@ -485,7 +602,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
 
     const int tok = kPlanes == 2 ? n & 7 : n;
     const half8* mine = xs + (kPlanes * min(tok, a.T - 1) + (kPlanes == 2 ? n >> 3 : 0)) * units + g;
-    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+    floatx4 acc2[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     for (int c0 = wave; c0 < chunks; c0 += kFewFlight * kRowWaves) {
 #pragma unroll
         for (int i = 0; i < kFewFlight; ++i) {
@@ -493,13 +610,13 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
             if (ch < chunks) {
 #pragma unroll
                 for (int c = 0; c < M::NCALL; ++c)
-                    acc = mfma::mfma(a_operand<BITS>(q[i], c), mine[(ch * M::NCALL + c) * 4], acc);
+                    acc2[c & 1] = mfma::mfma(a_operand<BITS>(q[i], c), mine[(ch * M::NCALL + c) * 4], acc2[c & 1]);
             }
             const int nx = ch + kFewFlight * kRowWaves;
             if (nx < chunks) q[i] = ld16(wrow + (int64_t)min(4 * nx + g, groups - 1) * 16);
         }
     }
-    part[wave][lane] = acc;
+    part[wave][lane] = acc2[0] + acc2[1];
     __syncthreads();
     if (wave != 0) return;
     floatx4 sum = part[0][lane];
@@ -515,11 +632,12 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
 
 // ------------------------------------------------------------------- launches
 
-constexpr int kRowsTokens = 64;           // linear_rows up to here
+constexpr int kRowsTokens = 32;           // linear_rows up to here
+constexpr int kCus = 256;
 
-bool few(const LinearArgs& a, int bits, int bytes) {
-    const int64_t n = a.T * padded(a.K, bits);
-    return a.T <= kFewTokens && n * (bytes == 4 ? 4 : 2) <= kFewLds && n / 8 <= kFewUnits * kRowWaves * kWave;
+bool few(int64_t T, int64_t K, int bits, int bytes) {
+    const int64_t n = T * padded(K, bits);
+    return T <= kFewTokens && n * (bytes == 4 ? 4 : 2) <= kFewLds && n / 8 <= kFewUnits * kRowWaves * kWave;
 }
 
 // One store of four outputs is possible.
@@ -528,52 +646,103 @@ bool whole4(const LinearArgs& a, int bytes) {
     return !(reinterpret_cast<uintptr_t>(a.y) & m) && !(a.ldy * bytes & m);
 }
 
-template <typename T, int BITS, int NB, int TB, int WN, int WT>
-void launch_gemm(const LinearArgs& a, const half8* hi, const half8* lo, const float* inv, int calls, hipStream_t st) {
-    const int64_t tiles = (int64_t)((a.N + WN * NB * 16 - 1) / (WN * NB * 16)) *
-                          ((a.T + WT * TB * 16 - 1) / (WT * TB * 16));
-    hipLaunchKernelGGL((linear_gemm<T, BITS, NB, TB, WN, WT>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                       dim3(WN * WT * kWave), 0, st, a, hi, lo, inv, calls, whole4(a, T::bytes));
+// The tile of linear_gemm (weight rows by tokens) and the parts of K.
+struct Tiling {
+    int rows, tokens, splits;
+};
+Tiling tiling(int64_t T, int64_t K, int64_t N, int bits) {
+    auto count = [&](int r, int t) { return ((N + r - 1) / r) * ((T + t - 1) / t); };
+    // the largest tile that still gives most compute units a workgroup; below
+    // that, K is split until they have one, at least 4 steps of 128 columns each
+    Tiling k;
+    if (count(256, 256) >= 200) k = {256, 256, 1};
+    else if (T > 64) k = {128, 128, 1};
+    else k = {128, 64, 1};
+    if (k.rows == 128) {
+        const int64_t tiles = count(k.rows, k.tokens), most = padded(K, bits) / 512;
+        // (two for the 128-token tile, whose workgroups are half as large)
+        const int64_t want = k.tokens == 128 ? 2 * kCus : kCus;
+        int64_t s = (want + tiles / 2) / tiles;
+        if (s > most) s = most;
+        k.splits = (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+    }
+    return k;
 }
 
-template <typename T, int BITS, int NU>
-void launch_prepare(const LinearArgs& a, half8* hi, half8* lo, float* inv, int calls, hipStream_t st) {
-    const int64_t grid = (blocks16(a.T) + 7) / 8 * 8 * (16 / (kPrepThreads / kWave));
-    hipLaunchKernelGGL((linear_prepare<T, BITS, NU>), dim3((unsigned)grid), dim3(kPrepThreads), 0, st,
+template <typename T, int BITS, int NB, int TB, int WN, int WT, int D>
+void launch_gemm(const LinearArgs& a, const half8* hi, const half8* lo, const float* inv, float* part, int calls,
+                 int splits, hipStream_t st) {
+    const int64_t tiles = (int64_t)((a.N + WN * NB * 16 - 1) / (WN * NB * 16)) *
+                          ((a.T + WT * TB * 16 - 1) / (WT * TB * 16)) * splits;
+    hipLaunchKernelGGL((linear_gemm<T, BITS, NB, TB, WN, WT, D>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                       dim3(WN * WT * kWave), 0, st, a, hi, lo, inv, part, calls, splits, whole4(a, T::bytes));
+    if (splits > 1) {
+        const int64_t blocks = ((a.N + 3) / 4 + kJoinThreads - 1) / kJoinThreads;
+        hipLaunchKernelGGL((linear_join<T>), dim3((unsigned)(blocks * a.T)), dim3(kJoinThreads), 0, st, a, inv, part,
+                           splits, whole4(a, T::bytes));
+    }
+}
+
+template <typename T, int BITS, int NU, int WPT>
+void launch_units(const LinearArgs& a, half8* hi, half8* lo, float* inv, int calls, hipStream_t st) {
+    const int64_t grid = (blocks16(a.T) + 7) / 8 * 8 * (16 / (kPrepThreads / kWave / WPT));
+    hipLaunchKernelGGL((linear_prepare<T, BITS, NU, WPT>), dim3((unsigned)grid), dim3(kPrepThreads), 0, st,
                        reinterpret_cast<const typename T::type*>(a.x), a.ldx, a.T, a.K, calls, hi, lo, inv);
+}
+
+// Four waves a token while that fills the compute units no more than a few times
+// over (4 us instead of 8 for 16 tokens of 6144 columns), else one.
+template <typename T, int BITS>
+void launch_prepare(const LinearArgs& a, half8* hi, half8* lo, float* inv, int calls, hipStream_t st) {
+    const int units = calls * 4;
+    if (a.T <= 1024) {
+        if (units <= 256) launch_units<T, BITS, 1, 4>(a, hi, lo, inv, calls, st);
+        else if (units <= 1024) launch_units<T, BITS, 4, 4>(a, hi, lo, inv, calls, st);
+        else launch_units<T, BITS, 0, 4>(a, hi, lo, inv, calls, st);
+    } else {
+        if (units <= 256) launch_units<T, BITS, 4, 1>(a, hi, lo, inv, calls, st);
+        else if (units <= 1024) launch_units<T, BITS, 16, 1>(a, hi, lo, inv, calls, st);
+        else launch_units<T, BITS, 0, 4>(a, hi, lo, inv, calls, st);
+    }
+}
+
+template <typename T, int BITS, int TB>
+void launch_rows(const LinearArgs& a, const half8* hi, const half8* lo, const float* inv, int calls, hipStream_t st) {
+    const bool whole = whole4(a, T::bytes);
+    // two row blocks a workgroup where that still gives every compute unit one
+    if (a.N >= kCus * 32)
+        hipLaunchKernelGGL((linear_rows<T, BITS, TB, 2>), dim3((a.N + 31) / 32), dim3(kRowWaves * kWave), 0, st, a, hi,
+                           lo, inv, calls, whole);
+    else
+        hipLaunchKernelGGL((linear_rows<T, BITS, TB, 1>), dim3((a.N + 15) / 16), dim3(kRowWaves * kWave), 0, st, a, hi,
+                           lo, inv, calls, whole);
 }
 
 template <typename T, int BITS>
 hipError_t launch_bits(const LinearArgs& a, hipStream_t st) {
     const int64_t Kp = padded(a.K, BITS);
     const int calls = (int)(Kp / 32);
-    const bool whole = whole4(a, T::bytes);
-    const dim3 rows((a.N + 15) / 16), rt(kRowWaves * kWave);
-    if (few(a, BITS, T::bytes)) {
+    if (few(a.T, a.K, BITS, T::bytes)) {
         const size_t lds = (size_t)a.T * Kp * (T::bytes == 4 ? 4 : 2);
-        hipLaunchKernelGGL((linear_few<T, BITS>), rows, rt, lds, st, a, calls, whole);
+        hipLaunchKernelGGL((linear_few<T, BITS>), dim3((a.N + 15) / 16), dim3(kRowWaves * kWave), lds, st, a, calls,
+                           whole4(a, T::bytes));
         return hipGetLastError();
     }
     const int64_t blocks = blocks16(a.T);
     half8* hi = reinterpret_cast<half8*>(a.workspace);
     half8* lo = hi + (T::bytes == 4 ? blocks * calls * kWave : 0);
     float* inv = reinterpret_cast<float*>(lo + blocks * calls * kWave);
-    if (calls <= 64) launch_prepare<T, BITS, 4>(a, hi, lo, inv, calls, st);
-    else if (calls <= 128) launch_prepare<T, BITS, 8>(a, hi, lo, inv, calls, st);
-    else if (calls <= 256) launch_prepare<T, BITS, 16>(a, hi, lo, inv, calls, st);
-    else launch_prepare<T, BITS, 0>(a, hi, lo, inv, calls, st);
-    if (a.T <= 16) hipLaunchKernelGGL((linear_rows<T, BITS, 1>), rows, rt, 0, st, a, hi, lo, inv, calls, whole);
-    else if (a.T <= 32) hipLaunchKernelGGL((linear_rows<T, BITS, 2>), rows, rt, 0, st, a, hi, lo, inv, calls, whole);
-    else if (a.T <= 48) hipLaunchKernelGGL((linear_rows<T, BITS, 3>), rows, rt, 0, st, a, hi, lo, inv, calls, whole);
-    else if (a.T <= kRowsTokens)
-        hipLaunchKernelGGL((linear_rows<T, BITS, 4>), rows, rt, 0, st, a, hi, lo, inv, calls, whole);
-    else {
-        // the largest tile that still gives most compute units a workgroup
-        const int64_t big = (int64_t)((a.N + 255) / 256) * ((a.T + 255) / 256);
-        const int64_t mid = (int64_t)((a.N + 127) / 128) * ((a.T + 127) / 128);
-        if (big >= 200) launch_gemm<T, BITS, 4, 8, 4, 2>(a, hi, lo, inv, calls, st);
-        else if (mid >= 200) launch_gemm<T, BITS, 4, 4, 2, 2>(a, hi, lo, inv, calls, st);
-        else launch_gemm<T, BITS, 2, 2, 2, 2>(a, hi, lo, inv, calls, st);
+    float* part = inv + blocks * 16;
+    launch_prepare<T, BITS>(a, hi, lo, inv, calls, st);
+    if (a.T <= 16) {
+        launch_rows<T, BITS, 1>(a, hi, lo, inv, calls, st);
+    } else if (a.T <= kRowsTokens) {
+        launch_rows<T, BITS, 2>(a, hi, lo, inv, calls, st);
+    } else {
+        const Tiling k = tiling(a.T, a.K, a.N, BITS);
+        if (k.rows == 256) launch_gemm<T, BITS, 4, 8, 4, 2, 2>(a, hi, lo, inv, part, calls, k.splits, st);
+        else if (k.tokens == 128) launch_gemm<T, BITS, 4, 4, 2, 2, 2>(a, hi, lo, inv, part, calls, k.splits, st);
+        else launch_gemm<T, BITS, 1, 4, 8, 1, 4>(a, hi, lo, inv, part, calls, k.splits, st);
     }
     return hipGetLastError();
 }
@@ -590,12 +759,20 @@ hipError_t launch_type(int bits, const LinearArgs& a, hipStream_t st) {
 
 }  // namespace
 
-int64_t linear_workspace(int dtype, int64_t T, int64_t K) {
-    if (T == 0) return 0;
-    return blocks16(T) * 16 * (padded(K, 2) * (dtype == MOEDEC_F32 ? 4 : 2) + 4);
+int64_t linear_workspace(int bits, int dtype, int64_t T, int64_t K, int64_t N) {
+    const int bytes = dtype == MOEDEC_F32 ? 4 : 2;
+    if (T == 0 || few(T, K, bits, bytes)) return 0;
+    int64_t n = blocks16(T) * 16 * (padded(K, bits) * bytes + 4);
+    if (T > kRowsTokens) {
+        const int splits = tiling(T, K, N, bits).splits;
+        if (splits > 1) n += splits * T * ((N + 3) / 4 * 16);
+    }
+    return n;
 }
 
-int64_t linear_grid(const LinearArgs& a) { return (int64_t)((a.N + 63) / 64) * ((a.T + 63) / 64) + 8; }
+int64_t linear_grid(const LinearArgs& a) {
+    return (int64_t)((a.N + 127) / 128) * ((a.T + 63) / 64) * 16 + (int64_t)a.T * ((a.N + 1023) / 1024) + 8;
+}
 
 hipError_t launch_linear(int bits, int dtype, const LinearArgs& a, hipStream_t st) {
     if (a.T == 0) return hipSuccess;

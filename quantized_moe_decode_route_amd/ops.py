@@ -9,6 +9,7 @@ fallback: if libmoedec.so is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 from dataclasses import dataclass
@@ -80,7 +81,7 @@ for _b in ("q4", "q8", "q2"):
                                              _P, _P], _I)
     _SIGS[f"dense_linear_{_b}"] = ([_P, _I, _I64, _P, _P, _P, _I, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P],
                                    _I)
-_SIGS["dense_linear_workspace"] = ([_I, _I64, _I64], _I64)
+_SIGS["dense_linear_workspace"] = ([_I, _I, _I64, _I64, _I64], _I64)
 _SIGS["kv4_append"] = ([_P, _I, _P, _I64, _P, _I64, _I, _I64, _P, _P, _P], _I)
 _SIGS["kv4_read"] = ([_P, _I, _P, _P, _I64, _P, _I64, _P, _I64, _I, _P], _I)
 _SIGS["kv4_attention_workspace"] = ([_P, _I64, _I, _I64], _I64)
@@ -408,13 +409,23 @@ KV4_MAX_SEQS = 1024
 
 def _launch(name: str, dev: torch.device, *args) -> None:
     """The call on dev's current stream (its last argument), dev made current."""
-    fn = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    fn = getattr(_lib or lib(), name)
+    index = dev.index
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(name, st)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        _check(name, st)
+
+
+def _gpu_of(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    return t.device
 
 
 def _rows(t: torch.Tensor, inner: tuple, name: str, dev: torch.device) -> tuple[int, int]:
@@ -425,23 +436,29 @@ def _rows(t: torch.Tensor, inner: tuple, name: str, dev: torch.device) -> tuple[
         raise ValueError(f"{name} must be on {dev} (a GPU)")
     if t.dtype not in DTYPES:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    if t.dim() != 1 + len(inner) or tuple(t.shape[1:]) != inner:
-        raise ValueError(f"{name} must be [rows, {', '.join(map(str, inner))}], got {tuple(t.shape)}")
-    row, need = 1, t.stride()
+    shape = t.shape
+    if len(shape) != 1 + len(inner) or shape[1:] != inner:
+        raise ValueError(f"{name} must be [rows, {', '.join(map(str, inner))}], got {tuple(shape)}")
+    row = math.prod(inner)
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    ld, step = t.stride(), 1
     for i in range(len(inner), 0, -1):
-        if inner[i - 1] != 1 and need[i] != row:
+        if inner[i - 1] != 1 and ld[i] != step:
             raise ValueError(f"the rows of {name} must be contiguous")
-        row *= inner[i - 1]
-    return t.data_ptr(), (need[0] if t.shape[0] > 1 else row)
+        step *= inner[i - 1]
+    return t.data_ptr(), (ld[0] if shape[0] > 1 else row)
 
 
 def _on(t: torch.Tensor, dtype: torch.dtype, name: str, dev: torch.device, shape: tuple) -> int:
-    p = _dev(t, dtype, name)
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    if tuple(t.shape) != shape:
+    """Pointer of a contiguous tensor of that type, device and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
+            and t.is_contiguous()):
+        _dev(t, dtype, name)
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return p
+    return t.data_ptr()
 
 
 @dataclass
@@ -468,8 +485,9 @@ def linear(x: torch.Tensor, lin: Linear, act: str = "none", residual: torch.Tens
     may be residual).  act: none, silu, gelu (erf), relu."""
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    suffix, dev = _suffix(lin.bits), x.device
-    K, N = lin.n_in, lin.n_out
+    suffix, dev = _suffix(lin.bits), _gpu_of(x, "x")
+    N, nb = lin.q.shape
+    K = nb * 8 // lin.bits
     xp, ldx = _rows(x, (K,), "x", dev)
     T = x.shape[0]
     if out is None:
@@ -480,14 +498,14 @@ def linear(x: torch.Tensor, lin: Linear, act: str = "none", residual: torch.Tens
         raise ValueError("x, residual and out must have one dtype")
     if out.shape[0] != T or (residual is not None and residual.shape[0] != T):
         raise ValueError("residual and out must have x's rows")
-    wp = _on(lin.q, torch.uint8, "q", dev, (N, lin.q.shape[1]))
+    wp = _on(lin.q, torch.uint8, "q", dev, (N, nb))
     sp = _on(lin.scale, torch.float32, "scale", dev, (N,))
     bp = None if lin.bias is None else _on(lin.bias, torch.float32, "bias", dev, (N,))
     dt = DTYPES[x.dtype]
-    nb = lib().dense_linear_workspace(dt, T, K)
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb > 0 else None
+    need = lib().dense_linear_workspace(lin.bits, dt, T, K, N)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
     _launch(f"dense_linear_{suffix}", dev, xp, dt, ldx, wp, sp, bp, ACTS[act], rp, ldr, yp, ldy, T, K, N,
-            ws.data_ptr() if nb > 0 else None, max(nb, 0))
+            ws.data_ptr() if need > 0 else None, max(need, 0))
     return out
 
 
@@ -535,6 +553,8 @@ class KvCache:
 
     def struct(self) -> _KvCache:
         dev, (L, P, nb), (S, mp) = self.device, self.data.shape, self.table.shape
+        if dev.type != "cuda":
+            raise ValueError("the cache must be on the GPU")
         if nb != self.kv_heads * self.page_tokens * (self.head_dim + 8):
             raise ValueError(f"data has {nb} bytes a page, expected kv_heads * page_tokens * (head_dim + 8)")
         return _KvCache(L, P, self.page_tokens, self.kv_heads, self.head_dim, S, mp,

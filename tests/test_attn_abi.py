@@ -126,9 +126,10 @@ def test_bad_linear(lib, bits):
         assert call(**bad) == 1, bad
     assert call(K=1 << 17, ldx=1 << 17) == 2 and call(T=1 << 24) == 2 and call(N=1 << 24, ldy=1 << 24) == 2
     assert call(T=0, x=None, y=None) == 0
-    need = lib.dense_linear_workspace(0, 300, 128)
+    need = lib.dense_linear_workspace(bits, 0, 300, 128, 8)
     assert need > 0 and call(T=300, nb=need - 1) == 1 and call(T=300, ws=None, nb=need) == 1
-    assert lib.dense_linear_workspace(5, 1, 128) == -1 and lib.dense_linear_workspace(0, -1, 128) == -1
+    for sizes in ((4, 5, 1, 128, 8), (4, 0, -1, 128, 8), (3, 0, 1, 128, 8), (4, 0, 1, 1 << 17, 8), (4, 0, 1, 128, 0)):
+        assert lib.dense_linear_workspace(*sizes) == -1
 
 
 def test_binding_refuses(lib):
