@@ -8,17 +8,26 @@
 // token; 16 rows that share a key/value head are the N side of the products
 // (B operand), 32 keys at a time the M side of S^T = K Q^T and the K side of
 // O^T = V^T P^T.  In S^T a lane holds one row (lane % 16) and, with the tokens
-// of a 32-key tile given to the two 16-key MFMAs as 8*(r/4) + 4*t + r%4, keys
+// of a 32-key step given to the two 16-key MFMAs as 8*(r/4) + 4*t + r%4, keys
 // 8*(lane/16) .. +7: exactly the K-values its B operand of the second product
 // needs.  So probabilities never leave their lane, and the running maximum, the
 // sum and the rescaling of the accumulators are per-lane scalars.
+//
+// A workgroup owns NT * 16 rows and a stretch of keys, its four waves take every
+// fourth 32-key step, so a code is converted once per workgroup however many rows
+// it serves: NT = 1 for single tokens, 2 and 4 for drafts and prompts.  Bound by
+// HBM for few rows (each step's 32 * (head_dim + 8) bytes are loaded one step
+// ahead), by the vector ALUs for many (about 150 instructions a step for the
+// codes and 75 a row tile for the softmax, against 16 MFMAs of 16 cycles a row
+// tile at head_dim 128).
 //
 // Queries enter as fp16 under one power of two per row: exact for fp16 and bf16,
 // as a hi/lo pair (22 bits) for fp32.  The probabilities times their value scale
 // enter the second product as fp16 (fp32: again as a pair) under one power of two
 // per wave that follows the largest value scale seen.  For 16-bit activations the
 // rounding of a probability to fp16 (2^-12 relative) is below that of the output.
-// Scores, maxima, sums and accumulators are fp32.
+// Scores, maxima, sums and accumulators are fp32.  The maximum is a reference,
+// moved (with a rescaling) only when a score passes it by a factor of 2^8.
 #include "attn.h"
 
 namespace moedec {
@@ -28,13 +37,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kRows = 16;                 // rows (query heads of tokens) of a tile
 constexpr int kKeys = 32;                 // keys of a wave's step
+constexpr int kRound = kKeys * kWaves;    // keys of a round of the workgroup
 constexpr int kMinChunk = 256;            // keys of a split at least
 constexpr int kMaxSplits = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kFltMax = 3.402823466e38f;
+constexpr float kSlack = 8.f;             // log2 by which a score may pass the reference
 
 __device__ __forceinline__ floatx4 mfma16(const half8& a, const half8& b, const floatx4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -45,321 +56,469 @@ __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) <
 
 // Exponent k with m * 2^k in [2^14, 2^15) (0 for zero and non-finite m).
 __device__ __forceinline__ int row_exponent(float m) {
-    if (!(m > 0.f) || !(m <= 3.402823466e38f)) return 0;
+    if (!(m > 0.f) || !(m <= kFltMax)) return 0;
     const int e = (int)(__float_as_uint(m) >> 23) - 127;        // -127 for subnormals
     const int k = 14 - e;
     return k > 120 ? 120 : k;
 }
 
-// A row tile: rows [r0, r0 + 16) of sequence s's m * group rows (row = token *
+template <int N>
+struct Words {
+    uint32_t w[N];
+};
+// N consecutive words, in 16- or 8-byte loads (N even, p aligned to them).
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const uint32_t* p) {
+    Words<N> o;
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const u32x4 v = reinterpret_cast<const u32x4*>(p)[i];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o.w[4 * i + k] = v[k];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const uint2 v = reinterpret_cast<const uint2*>(p)[i];
+            o.w[2 * i] = v.x;
+            o.w[2 * i + 1] = v.y;
+        }
+    }
+    return o;
+}
+
+// A row tile: rows [r0, r0 + rt) of sequence s's m * group rows (row = token *
 // group + head of the group), and the keys [lo, hi) that any of them sees.
 struct Tile {
-    int s, q0, m, len, r0, lo, hi, per;
+    int s, q0, n, m, len, r0, lo, hi, per;
+    int full0, full1;                    // keys [full0, full1) are seen by every row of the tile
     bool any;
 };
 
-__device__ __forceinline__ Tile find_tile(const Cache& c, const AttnArgs& a, int slot, int splits) {
+__device__ __forceinline__ Tile find_tile(const Cache& c, const AttnArgs& a, int slot, int splits, int rt) {
     Tile t;
     const int group = a.heads / c.kv_heads;
-    t.s = seq_of_slot(a.q_start, c.n_seqs, a.rows, group, kRows, 1, slot);
+    t.s = seq_of_slot(a.q_start, c.n_seqs, a.rows, group, rt, 1, slot);
     const Span q = span_of(a.q_start, t.s, a.rows);
     t.q0 = q.q0;
-    const int n = q.q1 - q.q0;
-    t.m = a.granted ? min(n, max(a.granted[t.s], 0)) : n;
+    t.n = q.q1 - q.q0;
+    t.m = a.granted ? min(t.n, max(a.granted[t.s], 0)) : t.n;
     t.len = c.held(t.s);
-    t.r0 = (slot - slot_base(a.q_start, t.s, a.rows, group, kRows, 1)) * kRows;
-    t.any = t.r0 < n * group;
+    t.r0 = (slot - slot_base(a.q_start, t.s, a.rows, group, rt, 1)) * rt;
+    t.any = t.r0 < t.n * group;
     const int first = t.len - t.m + t.r0 / group;                            // position of the first row
-    const int last = t.len - t.m + min(t.r0 + kRows - 1, t.m * group - 1) / group;
+    const int last = t.len - t.m + min(t.r0 + rt - 1, t.m * group - 1) / group;
     t.hi = t.r0 < t.m * group ? max(last + 1, 0) : 0;
     t.lo = a.window > 0 ? max(first - a.window + 1, 0) & ~(kKeys - 1) : 0;
     if (t.hi < t.lo) t.hi = t.lo;
+    t.full1 = first + 1;
+    t.full0 = a.window > 0 ? last - a.window + 1 : 0;
     const int each = (t.hi - t.lo + splits - 1) / splits;
-    t.per = max(kMinChunk, (each + kKeys * kWaves - 1) / (kKeys * kWaves) * (kKeys * kWaves));
+    t.per = max(kMinChunk, (each + kRound - 1) / kRound * kRound);
     return t;
 }
 
 // One split of one tile of one key/value head.
-template <typename T, int D, bool kPair>
-__global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Cache c, AttnArgs a, int splits) {
+template <typename T, int D, int NT>
+__global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, AttnArgs a, int splits) {
+    constexpr bool kPair = T::bytes == 4;
+    constexpr int kP = kPair ? 2 : 1;
     constexpr int kS = D / 32;            // MFMAs of a score, K side
     constexpr int kH = D / 64;            // 64-column parts of the output
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    constexpr int kRT = 16 * NT;
+    constexpr int kLd = D + 4;
+    __shared__ half8 qs[NT][kS][kP][kWave];
+    __shared__ float so[kRT][kLd];
+    __shared__ float scm[kRT], sm[kWaves][kRT], sl[kWaves][kRT];
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
-    const int sp = blockIdx.x % splits, head = (blockIdx.x / splits) % c.kv_heads;
-    const int slot = blockIdx.x / splits / c.kv_heads;
+    const int head = blockIdx.x % c.kv_heads, sp = blockIdx.x / c.kv_heads % splits;
+    const int slots = gridDim.x / c.kv_heads / splits;
+    const int slot = slots - 1 - (int)(blockIdx.x / c.kv_heads / splits);    // the longest tiles of a prompt first
     const int group = a.heads / c.kv_heads;
-    const Tile t = find_tile(c, a, slot, splits);
+    const Tile t = find_tile(c, a, slot, splits, kRT);
     if (!t.any) return;
     const int k0 = t.lo + sp * t.per, k1 = min(t.hi, k0 + t.per);
     if (sp > 0 && k0 >= t.hi) return;
+    const int rows = t.m * group;          // rows that count
 
-    // this lane's row, its position and the keys it sees
-    const int row = t.r0 + n, tok = row / group;
-    const bool on = row < t.m * group;
-    const int pos = t.len - t.m + tok;
-    const int see1 = on ? pos + 1 : 0, see0 = a.window > 0 ? pos - a.window + 1 : 0;
-    const int64_t r_at = (int64_t)(t.q0 + tok);
-    const int qh = head * group + row % group;
-
-    half8 qhi[kS], qlo[kPair ? kS : 1];
-    float cm;                              // score (codes times q in fp16) -> log2 domain
-    {
-        float x[kS][8];
+    // The queries, one 16-row block a wave, to LDS in operand order; cm turns a
+    // score of codes and fp16 queries into log2 units (its sign is the queries').
+    for (int nt = wave; nt < NT; nt += kWaves) {
+        const int row = t.r0 + 16 * nt + n;
+        const bool on = row < rows;
+        const typename T::type* src = reinterpret_cast<const typename T::type*>(a.q) +
+                                      (int64_t)(t.q0 + (on ? row / group : 0)) * a.ldq +
+                                      (int64_t)(head * group + (on ? row % group : 0)) * D + 8 * g;
+        float x[kS][8], m = 0.f;
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
+            load8<T>(src + 32 * s, x[s]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[s][e] = 0.f;
-            if (on)
-                load8<T>(reinterpret_cast<const typename T::type*>(a.q) + r_at * a.ldq + (int64_t)qh * D + 32 * s + 8 * g,
-                         x[s]);
+            for (int e = 0; e < 8; ++e) {
+                if (!on) x[s][e] = 0.f;
+                m = fmaxf(m, fabsf(x[s][e]));
+            }
         }
-        float m = 0.f;
-#pragma unroll
-        for (int s = 0; s < kS; ++s)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[s][e]));
         m = fmaxf(m, __shfl_xor(m, 16, kWave));
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
         const int k = row_exponent(m);
-        const float f = pow2(k);
+        const float f = a.scale < 0.f ? -pow2(k) : pow2(k);
 #pragma unroll
-        for (int s = 0; s < kS; ++s)
+        for (int s = 0; s < kS; ++s) {
+            half8 h, l;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float v = x[s][e] * f;
-                asm volatile("" : "+v"(v));
-                const _Float16 h = (_Float16)v;
-                qhi[s][e] = h;
-                if (kPair) qlo[s][e] = (_Float16)(v - (float)h);
+                if (kPair) asm volatile("" : "+v"(v));          // one rounding for both halves
+                const _Float16 hv = (_Float16)v;
+                h[e] = hv;
+                l[e] = (_Float16)(v - (float)hv);
             }
-        cm = pow2(-k) * a.scale * kLog2e;
+            qs[nt][s][0][lane] = h;
+            if (kPair) qs[nt][s][kP - 1][lane] = l;
+        }
+        if (g == 0) scm[16 * nt + n] = pow2(-k) * fabsf(a.scale) * kLog2e;
     }
-
-    floatx4 acc[kH][4];
-#pragma unroll
-    for (int h = 0; h < kH; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[h][i] = floatx4{0.f, 0.f, 0.f, 0.f};
-    float M = kNegInf, L = 0.f;
-    float vref = 0x1p-100f, vinv = 0x1p105f;       // value scales enter as s_v * vinv <= 2^6, vinv = 2^5 / vref
 
     const int pt = c.page_tokens();
     const int32_t* row_pages = c.table + (int64_t)t.s * c.max_pages;
-    for (int j0 = k0 + wave * kKeys; j0 < k1; j0 += kWaves * kKeys) {
-        const int page = row_pages[j0 >> c.pt_log2];
-        if (!c.good(page)) continue;
-        const uint8_t* unit = c.unit(a.layer, page, head);
-        const int at = j0 & (pt - 1);
-        uint32_t kw[2][kS], vw[kH][4];
-        float ks[8], vs[8];
+    const int first = k0 + wave * kKeys;
+    const int steps = first < k1 ? (k1 - first + kRound - 1) / kRound : 0;
+    // lane i: the page of step 64*k + i
+    auto load_pages = [&](int step) {
+        const int j = first + (step + lane) * kRound;
+        return step + lane < steps ? row_pages[j >> c.pt_log2] : -1;
+    };
+    const uint8_t* base = c.data + (int64_t)a.layer * c.n_pages * c.page_bytes() + head * c.unit_bytes();
+    auto unit_of = [&](int page) { return base + (int64_t)page * c.page_bytes(); };
+    Words<kS> kw[2];                       // codes and scales of a step's keys: loaded a step ahead
+    Words<8> ks;
+    auto load_keys = [&](int page, int step) {
+        const uint8_t* unit = unit_of(page);
+        const int at = (first + step * kRound) & (pt - 1);
 #pragma unroll
         for (int tl = 0; tl < 2; ++tl) {
             const int kt = at + 8 * (n >> 2) + 4 * tl + (n & 3);
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(unit) + kt * (D / 8) + g * kS;
-#pragma unroll
-            for (int s = 0; s < kS; ++s) kw[tl][s] = p[s];
+            kw[tl] = load_words<kS>(reinterpret_cast<const uint32_t*>(unit) + kt * (D / 8) + g * kS);
         }
-        const uint32_t* vp = reinterpret_cast<const uint32_t*>(unit + (int64_t)pt * (D / 2)) + ((at >> 3) + g) * D + 4 * n;
+        ks = load_words<8>(reinterpret_cast<const uint32_t*>(unit + pt * D) + at + 8 * g);
+    };
+
+    int pages = load_pages(0);
+    int page = steps > 0 ? __builtin_amdgcn_readlane(pages, 0) : -1;
+    if (c.good(page)) load_keys(page, 0);
+    __syncthreads();                       // queries staged
+    float cm[NT], M[NT], L[NT];            // M: reference score, L: this lane's part of the sum
+    int see0[NT], see1[NT];
+    floatx4 acc[NT][kH][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int row = t.r0 + 16 * i + n, pos = t.len - t.m + row / group;
+        cm[i] = scm[16 * i + n];
+        M[i] = kNegInf;
+        L[i] = 0.f;
+        see1[i] = row < rows ? pos + 1 : 0;
+        see0[i] = a.window > 0 ? pos - a.window + 1 : 0;
 #pragma unroll
         for (int h = 0; h < kH; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vw[h][i] = vp[64 * h + i];
-        const float* ksp = reinterpret_cast<const float*>(unit + (int64_t)pt * D) + at + 8 * g;
-        const float* vsp = ksp + pt;
+            for (int j = 0; j < 4; ++j) acc[i][h][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    float vref = 0x1p-100f, vinv = 0x1p105f;       // value scales enter as s_v * vinv <= 2^5, vinv = 2^5 / vref
+
+    for (int step = 0; step < steps; ++step) {
+        int next = -1;
+        if (step + 1 < steps) {
+            if (((step + 1) & (kWave - 1)) == 0) pages = load_pages(step + 1);
+            next = __builtin_amdgcn_readlane(pages, (step + 1) & (kWave - 1));
+        }
+        if (!c.good(page)) {                       // positions that are not there
+            page = next;
+            if (c.good(page)) load_keys(page, step + 1);
+            continue;
+        }
+        const int j0 = first + step * kRound;
+        const bool edge = j0 < t.full0 || j0 + kKeys > t.full1;
+        Words<4> vw[kH];                           // this step's values: needed after the softmax
+        Words<8> vsw;
+        {
+            const uint8_t* unit = unit_of(page);
+            const int at = j0 & (pt - 1);
+            const uint32_t* vp = reinterpret_cast<const uint32_t*>(unit + pt * (D / 2)) + ((at >> 3) + g) * D + 4 * n;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            ks[e] = ksp[e];
-            vs[e] = vsp[e];
+            for (int h = 0; h < kH; ++h) vw[h] = load_words<4>(vp + 64 * h);
+            vsw = load_words<8>(reinterpret_cast<const uint32_t*>(unit + pt * (D + 4)) + at + 8 * g);
         }
 
-        floatx4 sc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        // scores: z[i][e] = s_k * (codes . q) of key j0 + 8*g + e, before cm
+        floatx4 sc[NT][2];
 #pragma unroll
-        for (int tl = 0; tl < 2; ++tl)
+        for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int s = 0; s < kS; ++s) {
-                const half8 kf = codes_f16(kw[tl][s]);
-                sc[tl] = mfma16(kf, qhi[s], sc[tl]);
-                if (kPair) sc[tl] = mfma16(kf, qlo[s], sc[tl]);
+        for (int s = 0; s < kS; ++s) {
+            const half8 kf0 = codes_f16(kw[0].w[s]), kf1 = codes_f16(kw[1].w[s]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int p = 0; p < kP; ++p) {
+                    const half8 q = qs[i][s][p][lane];
+                    sc[i][0] = mfma16(kf0, q, sc[i][0]);
+                    sc[i][1] = mfma16(kf1, q, sc[i][1]);
+                }
+        }
+        bool move = false;
+        float z[NT][8], mx[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            mx[i] = kNegInf;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                z[i][e] = sc[i][e >> 2][e & 3] * __uint_as_float(ks.w[e]);
+                if (edge) {
+                    const int key = j0 + 8 * g + e;
+                    if (!(key < see1[i] && key >= see0[i])) z[i][e] = kNegInf;
+                }
+                mx[i] = fmaxf(mx[i], z[i][e]);
             }
-        // scores of keys j0 + 8*g + e in the log2 domain; unseen keys are -inf
-        float z[8], mx = kNegInf, vmx = 0.f;
+            move = move || (mx[i] - M[i]) * cm[i] > kSlack || (M[i] == kNegInf && mx[i] > kNegInf);
+        }
+        page = next;
+        if (c.good(page)) load_keys(page, step + 1);
+        float vmx = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int key = j0 + 8 * g + e;
-            const bool seen = key < see1 && key >= see0;
-            z[e] = seen ? sc[e >> 2][e & 3] * ks[e] * cm : kNegInf;
-            mx = fmaxf(mx, z[e]);
-            if (key < t.hi) vmx = fmaxf(vmx, vs[e]);
+        for (int e = 0; e < 8; ++e)
+            if (!edge || j0 + 8 * g + e < t.hi) vmx = fmaxf(vmx, __uint_as_float(vsw.w[e]));
+        move = move || (vmx > vref && vmx <= kFltMax);
+        if (__ballot(move)) {
+            float vm = fmaxf(vmx, __shfl_xor(vmx, 16, kWave));
+            vm = fmaxf(vm, __shfl_xor(vm, 32, kWave));
+            float down = 1.f;
+            if (vm > vref && vm <= kFltMax) {      // a power of two above every scale so far
+                const float nr = pow2(min((int)(__float_as_uint(vm) >> 23) - 126, 126));
+                down = vref / nr;
+                vref = nr;
+                vinv = 0x1p5f / nr;
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                float m = fmaxf(mx[i], __shfl_xor(mx[i], 16, kWave));
+                m = fmaxf(m, __shfl_xor(m, 32, kWave));
+                const float Mn = fmaxf(M[i], m);
+                const float f = M[i] == kNegInf ? 0.f : exp2f((M[i] - Mn) * cm[i]);
+                L[i] *= f;
+                M[i] = Mn;
+#pragma unroll
+                for (int h = 0; h < kH; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][h][j] = acc[i][h][j] * (f * down);
+            }
         }
-        mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
-        vmx = fmaxf(vmx, __shfl_xor(vmx, 16, kWave));
-        vmx = fmaxf(vmx, __shfl_xor(vmx, 32, kWave));
-        const float Mn = fmaxf(M, mx);
-        const float base = Mn == kNegInf ? 0.f : Mn;
-        float f = M == kNegInf ? 0.f : exp2f(M - base);
-        L *= f;
-        if (vmx > vref && vmx <= 3.402823466e38f) {       // a power of two at least as large as every scale so far
-            const float nr = pow2(min((int)(__float_as_uint(vmx) >> 23) - 126, 126));
-            f *= vref / nr;
-            vref = nr;
-            vinv = 0x1p5f / nr;
+        float vs[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vs[e] = __uint_as_float(vsw.w[e]) * vinv;
+        half8 ph[NT], pl[kPair ? NT : 1];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const float ref = M[i] == kNegInf ? 0.f : M[i] * cm[i];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool unseen = edge && z[i][e] == kNegInf;
+                const float p = unseen ? 0.f : __builtin_amdgcn_exp2f(fmaf(z[i][e], cm[i], -ref));
+                L[i] += p;
+                float v = unseen ? 0.f : p * vs[e];              // an unseen key's scale may be anything
+                if (kPair) asm volatile("" : "+v"(v));
+                const _Float16 hv = (_Float16)v;
+                ph[i][e] = hv;
+                if (kPair) pl[i][e] = (_Float16)(v - (float)hv);
+            }
         }
-        M = Mn;
 #pragma unroll
         for (int h = 0; h < kH; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[h][i] = acc[h][i] * f;
-        half8 phi, plo;
+            for (int j = 0; j < 4; ++j) {
+                const half8 vf = codes_f16(vw[h].w[j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float p = exp2f(z[e] - base);
-            L += p;
-            float v = p > 0.f || p != p ? p * (vs[e] * vinv) : 0.f;     // an unseen key's scale may be anything
-            asm volatile("" : "+v"(v));
-            const _Float16 hv = (_Float16)v;
-            phi[e] = hv;
-            if (kPair) plo[e] = (_Float16)(v - (float)hv);
-        }
-#pragma unroll
-        for (int h = 0; h < kH; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const half8 vf = codes_f16(vw[h][i]);
-                acc[h][i] = mfma16(vf, phi, acc[h][i]);
-                if (kPair) acc[h][i] = mfma16(vf, plo, acc[h][i]);
+                for (int i = 0; i < NT; ++i) {
+                    acc[i][h][j] = mfma16(vf, ph[i], acc[i][h][j]);
+                    if (kPair) acc[i][h][j] = mfma16(vf, pl[i], acc[i][h][j]);
+                }
             }
     }
-    L += __shfl_xor(L, 16, kWave);
-    L += __shfl_xor(L, 32, kWave);
-    if (L != L) M = 0.f;                   // NaN scores only: not an empty row
 
-    // The four waves' parts under the common maximum: each wave's sum of the
-    // output lands in LDS, wave 0 .. 3 added in that order.
-    __shared__ float sm[kWaves][kRows], sl[kWaves][kRows];
-    __shared__ float so[kWaves][kRows][D + 4];
-    if (g == 0) {
-        sm[wave][n] = M;
-        sl[wave][n] = L;
+    // The four waves' parts under the common maximum, added in their order.
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        L[i] += __shfl_xor(L[i], 16, kWave);
+        L[i] += __shfl_xor(L[i], 32, kWave);
+        M[i] = M[i] == kNegInf ? kNegInf : M[i] * cm[i];
+        if (L[i] != L[i]) M[i] = 0.f;              // NaN scores only: not an empty row
+        if (g == 0) {
+            sm[wave][16 * i + n] = M[i];
+            sl[wave][16 * i + n] = L[i];
+        }
     }
     __syncthreads();
-    float Mx = kNegInf;
+    for (int w = 0; w < kWaves; ++w) {
+        if (wave == w) {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) Mx = fmaxf(Mx, sm[w][n]);
-    const float f = M == kNegInf ? 0.f : exp2f(M - Mx) * (vref * 0x1p-5f);
+            for (int i = 0; i < NT; ++i) {
+                float Mx = kNegInf;
 #pragma unroll
-    for (int h = 0; h < kH; ++h)
+                for (int k = 0; k < kWaves; ++k) Mx = fmaxf(Mx, sm[k][16 * i + n]);
+                const float f = M[i] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(M[i] - Mx) * (vref * 0x1p-5f);
+                // register r of the MFMA row 4*g + r is column 64*h + 4*(4*g + r) + j
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // register i of the MFMA's row 4*g + i' is column 64*h + 4*(4*g + i') + i
+                for (int h = 0; h < kH; ++h)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) so[wave][n][64 * h + 16 * g + 4 * r + i] = acc[h][i][r] * f;
+                    for (int r = 0; r < 4; ++r) {
+                        f32x4* o = reinterpret_cast<f32x4*>(&so[16 * i + n][64 * h + 16 * g + 4 * r]);
+                        f32x4 v = {acc[i][h][0][r] * f, acc[i][h][1][r] * f, acc[i][h][2][r] * f, acc[i][h][3][r] * f};
+                        if (w > 0) v += *o;
+                        *o = v;
+                    }
+            }
         }
-    __syncthreads();
-    float* wsf = reinterpret_cast<float*>(a.workspace);
-    for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-        const int m = i / (D / 4), col = i % (D / 4) * 4;
-        const int mrow = t.r0 + m;
-        if (splits > 1 && mrow >= t.m * group) continue;
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        __syncthreads();
+    }
+    constexpr int kQ = D / 4;              // float4 columns
+    for (int i = threadIdx.x; i < kRT * kQ; i += kThreads) {
+        const int m = i / kQ, col = i % kQ * 4, row = t.r0 + m;
+        if (row >= (splits > 1 ? rows : t.n * group)) break;
         float mm = kNegInf, l = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, sm[w][m]);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            l += sm[w][m] == kNegInf ? 0.f : sl[w][m] * exp2f(sm[w][m] - mm);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] += so[w][m][col + k];
-        }
+        for (int w = 0; w < kWaves; ++w)
+            l += sm[w][m] == kNegInf ? 0.f : sl[w][m] * __builtin_amdgcn_exp2f(sm[w][m] - mm);
+        f32x4 o = *reinterpret_cast<const f32x4*>(&so[m][col]);
         if (splits > 1) {
-            const int64_t part = ((int64_t)slot * c.kv_heads + head) * splits + sp;
-            float* base = wsf + part * (kRows * (D + 2));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) base[m * D + col + k] = o[k];
+            float* part = reinterpret_cast<float*>(a.workspace) +
+                          (((int64_t)slot * c.kv_heads + head) * splits + sp) * (kRT * (D + 2));
+            *reinterpret_cast<f32x4*>(part + m * D + col) = o;
             if (col == 0) {
-                base[kRows * D + m] = mm;
-                base[kRows * D + kRows + m] = l;
+                part[kRT * D + m] = mm;
+                part[kRT * D + kRT + m] = l;
             }
             continue;
         }
         // one split: the answer.  Rows outside the granted count give zeros.
-        const Span q = span_of(a.q_start, t.s, a.rows);
-        const int tk = mrow / group;
-        if (tk >= q.q1 - q.q0) continue;
-        const float inv = mm == kNegInf || mrow >= t.m * group ? 0.f : 1.0f / l;
+        const bool empty = mm == kNegInf || row >= rows;
+        const float inv = empty ? 0.f : 1.0f / l;
+        float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = inv == 0.f ? 0.f : o[k] * inv;
-        const int64_t at = (int64_t)(t.q0 + tk);
-        const int oh = head * group + mrow % group;
-        store4<T>(reinterpret_cast<typename T::type*>(a.out) + at * a.ldo + (int64_t)oh * D + col, o);
-        if (a.lse && col == 0) a.lse[at * a.heads + oh] = inv == 0.f ? kNegInf : mm * kLn2 + logf(l);
+        for (int k = 0; k < 4; ++k) v[k] = empty ? 0.f : o[k] * inv;
+        const int64_t at = (int64_t)(t.q0 + row / group);
+        const int oh = head * group + row % group;
+        store4<T>(reinterpret_cast<typename T::type*>(a.out) + at * a.ldo + (int64_t)oh * D + col, v);
+        if (a.lse && col == 0) a.lse[at * a.heads + oh] = empty ? kNegInf : (mm + log2f(l)) * kLn2;
     }
 }
 
-// Joins the splits of one tile of one key/value head: sum_s 2^(M_s - M) O_s.
+// Joins the splits of one row: sum_s 2^(M_s - M) O_s.  The threads take four
+// columns each and every few splits; LDS adds their sums in a fixed order.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void kv4_attention_join(Cache c, AttnArgs a, int splits) {
-    const int head = blockIdx.x % c.kv_heads, slot = blockIdx.x / c.kv_heads;
+__global__ __launch_bounds__(kThreads) void kv4_attention_join(Cache c, AttnArgs a, int splits, int rt) {
+    constexpr int kQ = D / 4, kG = kThreads / kQ;          // float4 columns, groups over the splits
+    __shared__ f32x4 so[kG][kQ];
+    __shared__ float sl[kG];
+    const int m = blockIdx.x % rt, head = blockIdx.x / rt % c.kv_heads, slot = blockIdx.x / rt / c.kv_heads;
     const int group = a.heads / c.kv_heads;
-    const Tile t = find_tile(c, a, slot, splits);
-    if (!t.any) return;
-    const Span q = span_of(a.q_start, t.s, a.rows);
+    const Tile t = find_tile(c, a, slot, splits, rt);
+    const int row = t.r0 + m;
+    if (!t.any || row >= t.n * group) return;
     const int used = max((t.hi - t.lo + t.per - 1) / t.per, 1);
+    const int64_t stride = (int64_t)rt * (D + 2);
     const float* parts = reinterpret_cast<const float*>(a.workspace) +
-                         ((int64_t)slot * c.kv_heads + head) * splits * (kRows * (D + 2));
-    for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-        const int m = i / (D / 4), col = i % (D / 4) * 4, mrow = t.r0 + m, tk = mrow / group;
-        if (tk >= q.q1 - q.q0) continue;
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-        float mm = kNegInf, l = 0.f;
-        const bool on = mrow < t.m * group;
-        if (on) {
-            for (int s = 0; s < used; ++s) mm = fmaxf(mm, parts[(int64_t)s * kRows * (D + 2) + kRows * D + m]);
-            for (int s = 0; s < used; ++s) {
-                const float* p = parts + (int64_t)s * kRows * (D + 2);
-                const float ms = p[kRows * D + m];
-                const float f = ms == kNegInf ? 0.f : exp2f(ms - mm);
-                l += ms == kNegInf ? 0.f : p[kRows * D + kRows + m] * f;
-                const f32x4 v = *reinterpret_cast<const f32x4*>(p + m * D + col);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] += ms == kNegInf ? 0.f : v[k] * f;
+                         ((int64_t)slot * c.kv_heads + head) * splits * stride;
+    const bool on = row < t.m * group;
+    const int q = threadIdx.x % kQ, k = threadIdx.x / kQ;
+    float mm = kNegInf;
+    if (on)
+        for (int s = threadIdx.x & (kWave - 1); s < used; s += kWave) mm = fmaxf(mm, parts[s * stride + rt * D + m]);
+    mm = wave_max(mm);                                     // every wave reads all of them
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+    if (on && mm > kNegInf && k < kG) {
+#pragma unroll 4
+        for (int s = k; s < used; s += kG) {
+            const float* p = parts + s * stride;
+            const float ms = p[rt * D + m], ls = p[rt * D + rt + m];
+            const f32x4 v = *reinterpret_cast<const f32x4*>(p + m * D + 4 * q);
+            const float f = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - mm);
+            if (f != 0.f) {                                // NaN parts count too
+                l += ls * f;
+                o += v * f;
             }
         }
-        const bool empty = !on || mm == kNegInf;
-        const float inv = empty ? 0.f : 1.0f / l;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = empty ? 0.f : o[k] * inv;
-        const int64_t at = (int64_t)(t.q0 + tk);
-        const int oh = head * group + mrow % group;
-        store4<T>(reinterpret_cast<typename T::type*>(a.out) + at * a.ldo + (int64_t)oh * D + col, o);
-        if (a.lse && col == 0) a.lse[at * a.heads + oh] = empty ? kNegInf : mm * kLn2 + logf(l);
     }
+    if (k < kG) {
+        so[k][q] = o;
+        if (q == 0) sl[k] = l;
+    }
+    __syncthreads();
+    if (threadIdx.x >= kQ) return;
+#pragma unroll
+    for (int i = 1; i < kG; ++i) {
+        o += so[i][q];
+        l += sl[i];
+    }
+    const bool empty = !on || mm == kNegInf;
+    const float inv = empty ? 0.f : 1.0f / l;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = empty ? 0.f : o[i] * inv;
+    const int64_t at = (int64_t)(t.q0 + row / group);
+    const int oh = head * group + row % group;
+    store4<T>(reinterpret_cast<typename T::type*>(a.out) + at * a.ldo + (int64_t)oh * D + 4 * q, v);
+    if (a.lse && q == 0) a.lse[at * a.heads + oh] = empty ? kNegInf : (mm + log2f(l)) * kLn2;
 }
 
-// Row tiles of a launch at most: a sequence of n rows owns floor-difference + 1 slots.
-int64_t tile_slots(const Cache& c, int rows, int heads) {
-    return (int64_t)rows * (heads / c.kv_heads) / kRows + c.n_seqs;
+// How a call is cut: 16-row blocks of a workgroup by the rows a sequence has on
+// average (the accumulators of four blocks fit the registers up to head_dim 128,
+// with fp32's pairs up to 64), and splits of the keys: enough workgroups for four
+// on every compute unit if the splits keep kMinChunk keys, and four times as many,
+// which evens out ragged lengths, if they keep four times that.
+struct Cut {
+    int nt, splits;
+    int64_t slots;
+};
+Cut cut_of(const Cache& c, int rows, int heads, int64_t max_len) {
+    Cut k;
+    const int64_t group = heads / c.kv_heads, total = rows * group;
+    const int64_t mean = total / c.n_seqs;
+    k.nt = mean <= 16 ? 1 : mean <= 32 || c.head_dim > 128 ? 2 : 4;
+    const int rt = 16 * k.nt;
+    k.slots = total / rt + c.n_seqs;                       // a sequence of n rows owns at least ceil(n / rt)
+    const int64_t busy = (total + rt - 1) / rt;
+    const int64_t base = (busy > c.n_seqs ? busy : rows < c.n_seqs ? rows : c.n_seqs) * c.kv_heads;
+    auto pieces = [&](int64_t want, int64_t chunk) {
+        const int64_t s = (want + base - 1) / base, most = (max_len + chunk - 1) / chunk;
+        return s < most ? s : most;
+    };
+    int64_t s = pieces(1024, kMinChunk);
+    const int64_t fine = pieces(4096, 4 * kMinChunk);
+    if (fine > s && k.nt < 4) s = fine;
+    k.splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+    return k;
 }
 
-// Splits of the keys: enough workgroups for two on every compute unit, none
-// shorter than kMinChunk keys.
-int split_count(const Cache& c, int rows, int heads, int64_t max_len) {
-    const int64_t base = (int64_t)rows * (heads / c.kv_heads) / kRows * c.kv_heads + c.kv_heads;
-    int64_t s = (4 * 256 + base - 1) / base;
-    const int64_t most = (max_len + kMinChunk - 1) / kMinChunk;
-    if (s > most) s = most;
-    return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+template <typename T, int D, int NT>
+void launch_tile(const Cache& c, const AttnArgs& a, const Cut& k, hipStream_t st) {
+    hipLaunchKernelGGL((kv4_attention_kernel<T, D, NT>), dim3((unsigned)(k.slots * c.kv_heads * k.splits)),
+                       dim3(kThreads), 0, st, c, a, k.splits);
 }
 
 template <typename T, int D>
 hipError_t launch_dim(const Cache& c, const AttnArgs& a, hipStream_t st) {
-    const int splits = split_count(c, a.rows, a.heads, a.max_len);
-    const int64_t tiles = tile_slots(c, a.rows, a.heads) * c.kv_heads;
-    hipLaunchKernelGGL((kv4_attention_kernel<T, D, T::bytes == 4>), dim3((unsigned)(tiles * splits)), dim3(kThreads), 0,
-                       st, c, a, splits);
-    if (splits > 1)
-        hipLaunchKernelGGL((kv4_attention_join<T, D>), dim3((unsigned)tiles), dim3(kThreads), 0, st, c, a, splits);
+    const Cut k = cut_of(c, a.rows, a.heads, a.max_len);
+    if (k.nt == 1) launch_tile<T, D, 1>(c, a, k, st);
+    else if (k.nt == 2) launch_tile<T, D, 2>(c, a, k, st);
+    else if constexpr (D <= 128) launch_tile<T, D, 4>(c, a, k, st);
+    if (k.splits > 1)
+        hipLaunchKernelGGL((kv4_attention_join<T, D>), dim3((unsigned)(k.slots * c.kv_heads * 16 * k.nt)),
+                           dim3(kThreads), 0, st, c, a, k.splits, 16 * k.nt);
     return hipGetLastError();
 }
 
@@ -377,13 +536,14 @@ hipError_t launch_type(const Cache& c, const AttnArgs& a, hipStream_t st) {
 }  // namespace
 
 int64_t attention_workspace(const Cache& c, int rows, int heads, int64_t max_len) {
-    const int splits = split_count(c, rows, heads, max_len);
-    if (splits == 1 || rows == 0) return 0;
-    return tile_slots(c, rows, heads) * c.kv_heads * splits * kRows * (c.head_dim + 2) * 4;
+    const Cut k = cut_of(c, rows, heads, max_len);
+    if (k.splits == 1 || rows == 0) return 0;
+    return k.slots * c.kv_heads * k.splits * (16 * k.nt) * (c.head_dim + 2) * 4;
 }
 
 int64_t attention_grid(const Cache& c, int rows, int heads, int64_t max_len) {
-    return tile_slots(c, rows, heads) * c.kv_heads * split_count(c, rows, heads, max_len);
+    const Cut k = cut_of(c, rows, heads, max_len);
+    return k.slots * c.kv_heads * (k.splits > 16 * k.nt ? k.splits : 16 * k.nt);
 }
 
 hipError_t launch_attention(const Cache& c, const AttnArgs& a, int dtype, hipStream_t st) {
