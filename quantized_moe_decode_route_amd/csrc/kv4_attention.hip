@@ -41,6 +41,7 @@ constexpr int kKeys = 32;                 // keys of a wave's step
 constexpr int kRound = kKeys * kWaves;    // keys of a round of the workgroup
 constexpr int kMinChunk = 256;            // keys of a split at least
 constexpr int kMaxSplits = 256;
+constexpr int kNoSplit = 768;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
@@ -49,6 +50,17 @@ constexpr float kSlack = 8.f;             // log2 by which a score may pass the 
 
 __device__ __forceinline__ floatx4 mfma16(const half8& a, const half8& b, const floatx4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// The largest of three, ignoring NaN: one instruction (fmaxf adds one per operand
+// whose bits come from memory, to quiet signalling NaNs).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float max8(const float* v) {
+    return max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), max3(v[6], v[7], v[7]));
 }
 
 // 2^k as a float, k in [-126, 127].
@@ -179,7 +191,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
             qs[nt][s][0][lane] = h;
             if (kPair) qs[nt][s][kP - 1][lane] = l;
         }
-        if (g == 0) scm[16 * nt + n] = pow2(-k) * fabsf(a.scale) * kLog2e;
+        // never 0: the score of an unseen key is -inf times cm
+        if (g == 0) scm[16 * nt + n] = fmaxf(pow2(-k) * fabsf(a.scale) * kLog2e, 0x1p-126f);
     }
 
     const int pt = c.page_tokens();
@@ -272,24 +285,28 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
         float z[NT][8], mx[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            mx[i] = kNegInf;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                z[i][e] = sc[i][e >> 2][e & 3] * __uint_as_float(ks.w[e]);
-                if (edge) {
+            for (int e = 0; e < 8; ++e) z[i][e] = sc[i][e >> 2][e & 3] * __uint_as_float(ks.w[e]);
+            if (edge) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
                     const int key = j0 + 8 * g + e;
-                    if (!(key < see1[i] && key >= see0[i])) z[i][e] = kNegInf;
+                    z[i][e] = key < see1[i] && key >= see0[i] ? z[i][e] : kNegInf;
                 }
-                mx[i] = fmaxf(mx[i], z[i][e]);
             }
+            mx[i] = max8(z[i]);
             move = move || (mx[i] - M[i]) * cm[i] > kSlack || (M[i] == kNegInf && mx[i] > kNegInf);
         }
         page = next;
         if (c.good(page)) load_keys(page, step + 1);
-        float vmx = 0.f;
+        float vs[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (!edge || j0 + 8 * g + e < t.hi) vmx = fmaxf(vmx, __uint_as_float(vsw.w[e]));
+        for (int e = 0; e < 8; ++e) vs[e] = __uint_as_float(vsw.w[e]);
+        if (edge) {                                // positions past the last key may hold anything
+#pragma unroll
+            for (int e = 0; e < 8; ++e) vs[e] = j0 + 8 * g + e < t.hi ? vs[e] : 0.f;
+        }
+        const float vmx = max8(vs);
         move = move || (vmx > vref && vmx <= kFltMax);
         if (__ballot(move)) {
             float vm = fmaxf(vmx, __shfl_xor(vmx, 16, kWave));
@@ -315,19 +332,18 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
                     for (int j = 0; j < 4; ++j) acc[i][h][j] = acc[i][h][j] * (f * down);
             }
         }
-        float vs[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vs[e] = __uint_as_float(vsw.w[e]) * vinv;
+        for (int e = 0; e < 8; ++e) vs[e] *= vinv;
         half8 ph[NT], pl[kPair ? NT : 1];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const float ref = M[i] == kNegInf ? 0.f : M[i] * cm[i];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const bool unseen = edge && z[i][e] == kNegInf;
-                const float p = unseen ? 0.f : __builtin_amdgcn_exp2f(fmaf(z[i][e], cm[i], -ref));
+                const float p = __builtin_amdgcn_exp2f(fmaf(z[i][e], cm[i], -ref));
                 L[i] += p;
-                float v = unseen ? 0.f : p * vs[e];              // an unseen key's scale may be anything
+                float v = p * vs[e];
+                if (edge) v = z[i][e] == kNegInf ? 0.f : v;      // an unseen key's scale may be NaN
                 if (kPair) asm volatile("" : "+v"(v));
                 const _Float16 hv = (_Float16)v;
                 ph[i][e] = hv;
@@ -416,72 +432,117 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
     }
 }
 
-// Joins the splits of one row: sum_s 2^(M_s - M) O_s.  The threads take four
-// columns each and every few splits; LDS adds their sums in a fixed order.
+// Joins the splits of a tile's rows: sum_s 2^(M_s - M) O_s.  A thread holds four
+// columns.  With up to kFewSplits parts the workgroup's kG thread groups take a
+// row each and all of its parts; with more they share a row, every kG-th part
+// each, and LDS adds their sums in a fixed order.  `per` workgroups a tile.  All
+// loads of a thread go out together: the launch is a few latencies long.
+constexpr int kFewSplits = 8;
+
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void kv4_attention_join(Cache c, AttnArgs a, int splits, int rt) {
-    constexpr int kQ = D / 4, kG = kThreads / kQ;          // float4 columns, groups over the splits
+__global__ __launch_bounds__(kThreads) void kv4_attention_join(Cache c, AttnArgs a, int splits, int rt, int per) {
+    constexpr int kQ = D / 4, kG = kThreads / kQ;          // float4 columns, groups
     __shared__ f32x4 so[kG][kQ];
-    __shared__ float sl[kG];
-    const int m = blockIdx.x % rt, head = blockIdx.x / rt % c.kv_heads, slot = blockIdx.x / rt / c.kv_heads;
+    __shared__ float sl[kG], sm[kG];
+    const int j = blockIdx.x % per, head = blockIdx.x / per % c.kv_heads, slot = blockIdx.x / per / c.kv_heads;
     const int group = a.heads / c.kv_heads;
     const Tile t = find_tile(c, a, slot, splits, rt);
-    const int row = t.r0 + m;
-    if (!t.any || row >= t.n * group) return;
+    if (!t.any) return;
     const int used = max((t.hi - t.lo + t.per - 1) / t.per, 1);
     const int64_t stride = (int64_t)rt * (D + 2);
     const float* parts = reinterpret_cast<const float*>(a.workspace) +
                          ((int64_t)slot * c.kv_heads + head) * splits * stride;
-    const bool on = row < t.m * group;
     const int q = threadIdx.x % kQ, k = threadIdx.x / kQ;
-    float mm = kNegInf;
-    if (on)
-        for (int s = threadIdx.x & (kWave - 1); s < used; s += kWave) mm = fmaxf(mm, parts[s * stride + rt * D + m]);
-    mm = wave_max(mm);                                     // every wave reads all of them
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    if (on && mm > kNegInf && k < kG) {
-#pragma unroll 4
-        for (int s = k; s < used; s += kG) {
-            const float* p = parts + s * stride;
-            const float ms = p[rt * D + m], ls = p[rt * D + rt + m];
-            const f32x4 v = *reinterpret_cast<const f32x4*>(p + m * D + 4 * q);
-            const float f = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - mm);
-            if (f != 0.f) {                                // NaN parts count too
-                l += ls * f;
-                o += v * f;
+    const int end = min(rt, t.n * group - t.r0), live = t.m * group - t.r0;      // rows to write, rows that count
+    auto put = [&](int m, const f32x4& o, float mm, float l) {
+        const int row = t.r0 + m;
+        const bool empty = m >= live || mm == kNegInf;
+        const float inv = empty ? 0.f : 1.0f / l;
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = empty ? 0.f : o[i] * inv;
+        const int64_t at = (int64_t)(t.q0 + row / group);
+        const int oh = head * group + row % group;
+        store4<T>(reinterpret_cast<typename T::type*>(a.out) + at * a.ldo + (int64_t)oh * D + 4 * q, v);
+        if (a.lse && q == 0) a.lse[at * a.heads + oh] = empty ? kNegInf : (mm + log2f(l)) * kLn2;
+    };
+    // up to kFewSplits parts first, first + step, ... of row m: their sum under their
+    // own maximum mm (a part without a key has M = -inf, L = 0, O = 0)
+    auto gather = [&](int m, int first, int step, f32x4& o, float& l, float& mm) {
+        float ms[kFewSplits], ls[kFewSplits];
+        f32x4 v[kFewSplits];
+#pragma unroll
+        for (int i = 0; i < kFewSplits; ++i) {
+            const float* p = parts + min(first + i * step, used - 1) * stride;
+            ms[i] = p[rt * D + m];
+            ls[i] = p[rt * D + rt + m];
+            v[i] = *reinterpret_cast<const f32x4*>(p + m * D + 4 * q);
+        }
+        float top = mm;
+#pragma unroll
+        for (int i = 0; i < kFewSplits; ++i) top = first + i * step < used ? fmaxf(top, ms[i]) : top;
+        const float ref = top == kNegInf ? 0.f : top, f0 = mm == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mm - ref);
+        o = o * f0;
+        l *= f0;
+#pragma unroll
+        for (int i = 0; i < kFewSplits; ++i) {
+            if (first + i * step >= used) break;
+            const float f = __builtin_amdgcn_exp2f(ms[i] - ref);
+            l += ls[i] * f;
+            o += v[i] * f;
+        }
+        mm = top;
+    };
+    if (used <= kFewSplits) {
+        if (k >= kG) return;
+        for (int m = j * kG + k; m < end; m += per * kG) {
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+            float l = 0.f, mm = kNegInf;
+            if (m < live) gather(m, 0, 1, o, l, mm);
+            put(m, o, mm, l);
+        }
+        return;
+    }
+    for (int m = j; m < end; m += per) {                   // the whole workgroup, row by row
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        float l = 0.f, mm = kNegInf;
+        if (m < live && k < kG)
+            for (int s = k; s < used; s += kG * kFewSplits) gather(m, s, kG, o, l, mm);
+        __syncthreads();                                   // the last row's sums are read
+        if (k < kG) {
+            so[k][q] = o;
+            if (q == 0) {
+                sl[k] = l;
+                sm[k] = mm;
             }
         }
-    }
-    if (k < kG) {
-        so[k][q] = o;
-        if (q == 0) sl[k] = l;
-    }
-    __syncthreads();
-    if (threadIdx.x >= kQ) return;
+        __syncthreads();
+        if (threadIdx.x < kQ) {
+            float top = kNegInf;
 #pragma unroll
-    for (int i = 1; i < kG; ++i) {
-        o += so[i][q];
-        l += sl[i];
-    }
-    const bool empty = !on || mm == kNegInf;
-    const float inv = empty ? 0.f : 1.0f / l;
-    float v[4];
+            for (int i = 0; i < kG; ++i) top = fmaxf(top, sm[i]);
+            o = f32x4{0.f, 0.f, 0.f, 0.f};
+            l = 0.f;
+            const float ref = top == kNegInf ? 0.f : top;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = empty ? 0.f : o[i] * inv;
-    const int64_t at = (int64_t)(t.q0 + row / group);
-    const int oh = head * group + row % group;
-    store4<T>(reinterpret_cast<typename T::type*>(a.out) + at * a.ldo + (int64_t)oh * D + 4 * q, v);
-    if (a.lse && q == 0) a.lse[at * a.heads + oh] = empty ? kNegInf : (mm + log2f(l)) * kLn2;
+            for (int i = 0; i < kG; ++i) {
+                const float f = __builtin_amdgcn_exp2f(sm[i] - ref);
+                o += so[i][q] * f;
+                l += sl[i] * f;
+            }
+            put(m, o, top, l);
+        }
+    }
 }
 
 // How a call is cut: 16-row blocks of a workgroup by the rows a sequence has on
 // average (the accumulators of four blocks fit the registers up to head_dim 128,
 // with fp32's pairs up to 64), and splits of the keys: enough workgroups for four
 // on every compute unit if the splits keep kMinChunk keys, and four times as many,
-// which evens out ragged lengths, if they keep four times that.
+// which evens out ragged lengths, if they keep eight times that.  Up to kNoSplit keys
+// the second launch would cost more than it saves.
 struct Cut {
-    int nt, splits;
+    int nt, splits, joins;
     int64_t slots;
 };
 Cut cut_of(const Cache& c, int rows, int heads, int64_t max_len) {
@@ -497,10 +558,12 @@ Cut cut_of(const Cache& c, int rows, int heads, int64_t max_len) {
         const int64_t s = (want + base - 1) / base, most = (max_len + chunk - 1) / chunk;
         return s < most ? s : most;
     };
-    int64_t s = pieces(1024, kMinChunk);
-    const int64_t fine = pieces(4096, 4 * kMinChunk);
+    int64_t s = max_len <= kNoSplit ? 1 : pieces(1024, kMinChunk);
+    const int64_t fine = pieces(4096, 8 * kMinChunk);
     if (fine > s && k.nt < 4) s = fine;
     k.splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+    // a workgroup a row where it shares the row's many parts, else one a few rows
+    k.joins = k.splits > kFewSplits ? rt : k.nt;
     return k;
 }
 
@@ -517,8 +580,8 @@ hipError_t launch_dim(const Cache& c, const AttnArgs& a, hipStream_t st) {
     else if (k.nt == 2) launch_tile<T, D, 2>(c, a, k, st);
     else if constexpr (D <= 128) launch_tile<T, D, 4>(c, a, k, st);
     if (k.splits > 1)
-        hipLaunchKernelGGL((kv4_attention_join<T, D>), dim3((unsigned)(k.slots * c.kv_heads * 16 * k.nt)),
-                           dim3(kThreads), 0, st, c, a, k.splits, 16 * k.nt);
+        hipLaunchKernelGGL((kv4_attention_join<T, D>), dim3((unsigned)(k.slots * c.kv_heads * k.joins)), dim3(kThreads),
+                           0, st, c, a, k.splits, 16 * k.nt, k.joins);
     return hipGetLastError();
 }
 
@@ -543,7 +606,7 @@ int64_t attention_workspace(const Cache& c, int rows, int heads, int64_t max_len
 
 int64_t attention_grid(const Cache& c, int rows, int heads, int64_t max_len) {
     const Cut k = cut_of(c, rows, heads, max_len);
-    return k.slots * c.kv_heads * (k.splits > 16 * k.nt ? k.splits : 16 * k.nt);
+    return k.slots * c.kv_heads * (k.splits > k.joins ? k.splits : k.joins);
 }
 
 hipError_t launch_attention(const Cache& c, const AttnArgs& a, int dtype, hipStream_t st) {
