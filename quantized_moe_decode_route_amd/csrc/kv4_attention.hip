@@ -155,6 +155,34 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
     if (sp > 0 && k0 >= t.hi) return;
     const int rows = t.m * group;          // rows that count
 
+    const int width = a.window > 0 ? a.window : 0x7FFFFFFF;     // see1 - width stays in range: see1 >= 0
+    const int pt = c.page_tokens();
+    const int32_t* row_pages = c.table + (int64_t)t.s * c.max_pages;
+    const int first = k0 + wave * kKeys;
+    const int steps = first < k1 ? (k1 - first + kRound - 1) / kRound : 0;
+    // lane i: the page of step 64*k + i
+    auto load_pages = [&](int step) {
+        const int j = first + (step + lane) * kRound;
+        return step + lane < steps ? row_pages[j >> c.pt_log2] : -1;
+    };
+    const uint8_t* base = c.data + (int64_t)a.layer * c.n_pages * c.page_bytes() + head * c.unit_bytes();
+    auto unit_of = [&](int page) { return base + (int64_t)page * c.page_bytes(); };
+    Words<kS> kw[2];                       // codes and scales of a step's keys: loaded a step ahead
+    Words<8> ks;
+    auto load_keys = [&](int page, int step) {
+        const uint8_t* unit = unit_of(page);
+        const int at = (first + step * kRound) & (pt - 1);
+#pragma unroll
+        for (int tl = 0; tl < 2; ++tl) {
+            const int kt = at + 8 * (n >> 2) + 4 * tl + (n & 3);
+            kw[tl] = load_words<kS>(reinterpret_cast<const uint32_t*>(unit) + kt * (D / 8) + g * kS);
+        }
+        ks = load_words<8>(reinterpret_cast<const uint32_t*>(unit + pt * D) + at + 8 * g);
+    };
+
+    int pages = load_pages(0);
+    int page = steps > 0 ? __builtin_amdgcn_readlane(pages, 0) : -1;
+    if (c.good(page)) load_keys(page, 0);
     // The queries, one 16-row block a wave, to LDS in operand order; cm turns a
     // score of codes and fp16 queries into log2 units (its sign is the queries').
     for (int nt = wave; nt < NT; nt += kWaves) {
@@ -195,36 +223,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
         if (g == 0) scm[16 * nt + n] = fmaxf(pow2(-k) * fabsf(a.scale) * kLog2e, 0x1p-126f);
     }
 
-    const int pt = c.page_tokens();
-    const int32_t* row_pages = c.table + (int64_t)t.s * c.max_pages;
-    const int first = k0 + wave * kKeys;
-    const int steps = first < k1 ? (k1 - first + kRound - 1) / kRound : 0;
-    // lane i: the page of step 64*k + i
-    auto load_pages = [&](int step) {
-        const int j = first + (step + lane) * kRound;
-        return step + lane < steps ? row_pages[j >> c.pt_log2] : -1;
-    };
-    const uint8_t* base = c.data + (int64_t)a.layer * c.n_pages * c.page_bytes() + head * c.unit_bytes();
-    auto unit_of = [&](int page) { return base + (int64_t)page * c.page_bytes(); };
-    Words<kS> kw[2];                       // codes and scales of a step's keys: loaded a step ahead
-    Words<8> ks;
-    auto load_keys = [&](int page, int step) {
-        const uint8_t* unit = unit_of(page);
-        const int at = (first + step * kRound) & (pt - 1);
-#pragma unroll
-        for (int tl = 0; tl < 2; ++tl) {
-            const int kt = at + 8 * (n >> 2) + 4 * tl + (n & 3);
-            kw[tl] = load_words<kS>(reinterpret_cast<const uint32_t*>(unit) + kt * (D / 8) + g * kS);
-        }
-        ks = load_words<8>(reinterpret_cast<const uint32_t*>(unit + pt * D) + at + 8 * g);
-    };
-
-    int pages = load_pages(0);
-    int page = steps > 0 ? __builtin_amdgcn_readlane(pages, 0) : -1;
-    if (c.good(page)) load_keys(page, 0);
     __syncthreads();                       // queries staged
     float cm[NT], M[NT], L[NT];            // M: reference score, L: this lane's part of the sum
-    int see0[NT], see1[NT];
+    int see1[NT];                          // keys [see1 - window, see1) are seen
     floatx4 acc[NT][kH][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -232,13 +233,14 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
         cm[i] = scm[16 * i + n];
         M[i] = kNegInf;
         L[i] = 0.f;
-        see1[i] = row < rows ? pos + 1 : 0;
-        see0[i] = a.window > 0 ? pos - a.window + 1 : 0;
+        see1[i] = row < rows ? max(pos + 1, 0) : 0;
 #pragma unroll
         for (int h = 0; h < kH; ++h)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][h][j] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
+    floatx4 zero = {0.f, 0.f, 0.f, 0.f};           // held in registers: the first product's addend
+    asm volatile("" : "+v"(zero));
     float vref = 0x1p-100f, vinv = 0x1p105f;       // value scales enter as s_v * vinv <= 2^5, vinv = 2^5 / vref
 
     for (int step = 0; step < steps; ++step) {
@@ -253,7 +255,6 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
             continue;
         }
         const int j0 = first + step * kRound;
-        const bool edge = j0 < t.full0 || j0 + kKeys > t.full1;
         Words<4> vw[kH];                           // this step's values: needed after the softmax
         Words<8> vsw;
         {
@@ -265,10 +266,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
             vsw = load_words<8>(reinterpret_cast<const uint32_t*>(unit + pt * (D + 4)) + at + 8 * g);
         }
 
-        // scores: z[i][e] = s_k * (codes . q) of key j0 + 8*g + e, before cm
+        const bool edge = j0 < t.full0 || j0 + kKeys > t.full1;    // some row does not see some key
+
+    // scores: z[i][e] = s_k * (codes . q) of key j0 + 8*g + e, before cm
         floatx4 sc[NT][2];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) sc[i][0] = sc[i][1] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
             const half8 kf0 = codes_f16(kw[0].w[s]), kf1 = codes_f16(kw[1].w[s]);
@@ -277,8 +278,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
                     const half8 q = qs[i][s][p][lane];
-                    sc[i][0] = mfma16(kf0, q, sc[i][0]);
-                    sc[i][1] = mfma16(kf1, q, sc[i][1]);
+                    sc[i][0] = mfma16(kf0, q, s == 0 && p == 0 ? zero : sc[i][0]);
+                    sc[i][1] = mfma16(kf1, q, s == 0 && p == 0 ? zero : sc[i][1]);
                 }
         }
         bool move = false;
@@ -288,10 +289,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[i][e] = sc[i][e >> 2][e & 3] * __uint_as_float(ks.w[e]);
             if (edge) {
+                asm volatile("");                  // a branch, not selects in every step
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int key = j0 + 8 * g + e;
-                    z[i][e] = key < see1[i] && key >= see0[i] ? z[i][e] : kNegInf;
+                    z[i][e] = key < see1[i] && key >= see1[i] - width ? z[i][e] : kNegInf;
                 }
             }
             mx[i] = max8(z[i]);
@@ -338,16 +340,24 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, Att
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const float ref = M[i] == kNegInf ? 0.f : M[i] * cm[i];
+            float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(z[i][e], cm[i], -ref));
                 L[i] += p;
-                float v = p * vs[e];
-                if (edge) v = z[i][e] == kNegInf ? 0.f : v;      // an unseen key's scale may be NaN
-                if (kPair) asm volatile("" : "+v"(v));
-                const _Float16 hv = (_Float16)v;
+                v[e] = p * vs[e];
+            }
+            if (edge) {                            // an unseen key's scale may be NaN
+                asm volatile("");
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = z[i][e] == kNegInf ? 0.f : v[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (kPair) asm volatile("" : "+v"(v[e]));
+                const _Float16 hv = (_Float16)v[e];
                 ph[i][e] = hv;
-                if (kPair) pl[i][e] = (_Float16)(v - (float)hv);
+                if (kPair) pl[i][e] = (_Float16)(v[e] - (float)hv);
             }
         }
 #pragma unroll
