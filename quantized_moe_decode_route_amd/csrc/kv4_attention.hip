@@ -15,7 +15,7 @@
 //
 // A workgroup owns NT * 16 rows and a stretch of keys, its four waves take every
 // fourth 32-key step, so a code is converted once per workgroup however many rows
-// it serves: NT = 1 for single tokens, 2 and 4 for drafts and prompts.  Bound by
+// it serves: NT = 1 for single tokens, 2 and 3 for drafts and prompts.  Bound by
 // HBM for few rows (each step's 32 * (head_dim + 8) bytes are loaded one step
 // ahead), by the vector ALUs for many (about 150 instructions a step for the
 // codes and 75 a row tile for the softmax, against 16 MFMAs of 16 cycles a row
@@ -131,9 +131,13 @@ __device__ __forceinline__ Tile find_tile(const Cache& c, const AttnArgs& a, int
     return t;
 }
 
+// Waves a SIMD is to hold (the register budget): as many as the accumulators allow
+// without spilling.
+constexpr int waves_per_simd(int D, int NT) { return D == 64 && NT <= 2 ? 4 : D <= 128 && NT == 1 ? 4 : 2; }
+
 // One split of one tile of one key/value head.
 template <typename T, int D, int NT>
-__global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Cache c, AttnArgs a, int splits) {
+__global__ __launch_bounds__(kThreads, waves_per_simd(D, NT)) void kv4_attention_kernel(Cache c, AttnArgs a, int splits) {
     constexpr bool kPair = T::bytes == 4;
     constexpr int kP = kPair ? 2 : 1;
     constexpr int kS = D / 32;            // MFMAs of a score, K side
@@ -546,8 +550,10 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_join(Cache c, AttnArgs
 }
 
 // How a call is cut: 16-row blocks of a workgroup by the rows a sequence has on
-// average (the accumulators of four blocks fit the registers up to head_dim 128,
-// with fp32's pairs up to 64), and splits of the keys: enough workgroups for four
+// average (prompts: three at head_dim 128, where four spilled registers, 614
+// against 587 us for 2 x 1500 queries of 48 heads over 6000 keys, and two
+// elsewhere: at 64 two with four waves a SIMD took 55 us for 3 x 1000 queries of 8
+// heads over 3000 keys, four with two waves 68), and splits of the keys: enough workgroups for four
 // on every compute unit if the splits keep kMinChunk keys, and four times as many,
 // which evens out ragged lengths, if they keep eight times that.  Up to kNoSplit keys
 // the second launch would cost more than it saves.
@@ -559,7 +565,7 @@ Cut cut_of(const Cache& c, int rows, int heads, int64_t max_len) {
     Cut k;
     const int64_t group = heads / c.kv_heads, total = rows * group;
     const int64_t mean = total / c.n_seqs;
-    k.nt = mean <= 16 ? 1 : mean <= 32 || c.head_dim > 128 ? 2 : 4;
+    k.nt = mean <= 16 ? 1 : mean <= 32 || c.head_dim != 128 ? 2 : 3;
     const int rt = 16 * k.nt;
     k.slots = total / rt + c.n_seqs;                       // a sequence of n rows owns at least ceil(n / rt)
     const int64_t busy = (total + rt - 1) / rt;
@@ -570,7 +576,7 @@ Cut cut_of(const Cache& c, int rows, int heads, int64_t max_len) {
     };
     int64_t s = max_len <= kNoSplit ? 1 : pieces(1024, kMinChunk);
     const int64_t fine = pieces(4096, 8 * kMinChunk);
-    if (fine > s && k.nt < 4) s = fine;
+    if (fine > s && mean <= 32) s = fine;
     k.splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
     // a workgroup a row where it shares the row's many parts, else one a few rows
     k.joins = k.splits > kFewSplits ? rt : k.nt;
@@ -588,7 +594,7 @@ hipError_t launch_dim(const Cache& c, const AttnArgs& a, hipStream_t st) {
     const Cut k = cut_of(c, a.rows, a.heads, a.max_len);
     if (k.nt == 1) launch_tile<T, D, 1>(c, a, k, st);
     else if (k.nt == 2) launch_tile<T, D, 2>(c, a, k, st);
-    else if constexpr (D <= 128) launch_tile<T, D, 4>(c, a, k, st);
+    else if constexpr (D == 128) launch_tile<T, D, 3>(c, a, k, st);
     if (k.splits > 1)
         hipLaunchKernelGGL((kv4_attention_join<T, D>), dim3((unsigned)(k.slots * c.kv_heads * k.joins)), dim3(kThreads),
                            0, st, c, a, k.splits, 16 * k.nt, k.joins);
