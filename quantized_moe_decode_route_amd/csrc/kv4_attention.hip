@@ -569,7 +569,8 @@ Cut cut_of(const Cache& c, int rows, int heads, int64_t max_len) {
     const int rt = 16 * k.nt;
     k.slots = total / rt + c.n_seqs;                       // a sequence of n rows owns at least ceil(n / rt)
     const int64_t busy = (total + rt - 1) / rt;
-    const int64_t base = (busy > c.n_seqs ? busy : rows < c.n_seqs ? rows : c.n_seqs) * c.kv_heads;
+    const int64_t tiles = busy > c.n_seqs ? busy : rows < c.n_seqs ? rows : c.n_seqs;
+    const int64_t base = (tiles < 1 ? 1 : tiles) * c.kv_heads;
     auto pieces = [&](int64_t want, int64_t chunk) {
         const int64_t s = (want + base - 1) / base, most = (max_len + chunk - 1) / chunk;
         return s < most ? s : most;

@@ -24,22 +24,23 @@ constexpr int kCopyUnroll = 4;
 constexpr int kCopyPart = kCopyThreads * 16 * kCopyUnroll;   // bytes a workgroup copies at a time
 constexpr int kCopyGrid = 2048;
 
-// Inclusive sum over the workgroup (every thread calls); the total in `total`.
-__device__ __forceinline__ int block_scan(int v, int* total) {
-    __shared__ int part[kWaves];
+// Inclusive sums over the workgroup (every thread calls), the totals in `total`.
+template <typename V>
+__device__ __forceinline__ V block_scan(V v, V* total) {
+    __shared__ V part[kWaves];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
-        const int u = __shfl_up(v, o, kWave);
+        const V u = __shfl_up(v, o, kWave);
         if (lane >= o) v += u;
     }
     __syncthreads();                               // the last call's readers are done
     if (lane == kWave - 1) part[wave] = v;
     __syncthreads();
-    int before = 0, all = 0;
+    V before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        const int p = part[w];
+        const V p = part[w];
         if (w < wave) before += p;
         all += p;
     }
@@ -64,15 +65,20 @@ __device__ __forceinline__ uint32_t free_mask(const Cache& c, int p) {
 }
 
 // One thread per sequence.  The copies to make: ws[0] their number, then the
-// source pages, then (from 1 + n_seqs) the destinations.
+// source pages, then (from 1 + n_seqs) the destinations.  The first step of the
+// free pages is read at once, beside the lengths: with up to 16384 pages the call
+// waits for memory three times and scans once.
 __global__ __launch_bounds__(kThreads) void kv4_reserve_kernel(Cache c, const int32_t* __restrict__ n_new,
                                                                int32_t* __restrict__ granted, int32_t* __restrict__ ws) {
-    __shared__ int part_page[kThreads];            // the shared, partly filled page a sequence is to write, or -1
-    __shared__ int end_of[kThreads];               // pages asked for by sequences 0 .. s
+    __shared__ int4 part_page4[kThreads / 4];      // the shared, partly filled page a sequence is to write, or -1
+    __shared__ int64_t end_of[kThreads];           // pages asked for by sequences 0 .. s
     __shared__ int place[kThreads];                // table column of the sequence's first place
-    __shared__ int copies[kThreads];               // its place in the list of copies, or -1
+    __shared__ int list[kStep];                    // the free pages of a step
+    __shared__ int copies[kThreads];               // the sequence's place in the list of copies, or -1
     __shared__ int refused, any_shared;
+    int* part_page = reinterpret_cast<int*>(part_page4);
     const int s = threadIdx.x, pt = c.page_tokens(), cap = c.max_pages << c.pt_log2;
+    const uint32_t mask0 = free_mask(c, min(s * kPer, c.n_pages));
     int len = 0, grow = 0, have = 0, want = 0, last = -1, refs = 0;
     if (s == 0) {
         refused = kThreads;
@@ -97,54 +103,75 @@ __global__ __launch_bounds__(kThreads) void kv4_reserve_kernel(Cache c, const in
     bool cow = false;
     if (any_shared && refs > 1) {
         int before = 0;
-        for (int j = 0; j < s; ++j) before += part_page[j] == last;
+        for (int j = 0; j < s; j += 4) {
+            const int4 v = part_page4[j / 4];
+            before += (v.x == last) + (j + 1 < s && v.y == last) + (j + 2 < s && v.z == last) +
+                      (j + 3 < s && v.w == last);
+        }
         cow = refs - before > 1;
     }
+    // one scan: pages asked for (under 2^36) and, above them, the copies among them
     const int need = want - have + (cow ? 1 : 0);
-    int total, got;
-    const int end = block_scan(need, &total);
+    int64_t sums;
+    const int64_t scan = block_scan<int64_t>((int64_t)need | (int64_t)cow << 48, &sums);
+    const int64_t end = scan & ((1ll << 48) - 1), total = sums & ((1ll << 48) - 1);
+    const int copies_to = (int)(scan >> 48);       // copies of sequences 0 .. s
     end_of[s] = end;
     place[s] = have - (cow ? 1 : 0);
     // enough free pages?
-    int found = 0;
+    int got, first0 = 0, first_got = 0;
+    int64_t found = 0;
     for (int base = 0; base < c.n_pages && found < total; base += kStep) {
-        block_scan(__popc(free_mask(c, min(base + s * kPer, c.n_pages))), &got);
+        const uint32_t m = base == 0 ? mask0 : free_mask(c, min(base + s * kPer, c.n_pages));
+        const int f = block_scan<int>(__popc(m), &got);
+        if (base == 0) {
+            first0 = f;
+            first_got = got;
+        }
         found += got;
     }
     if (grow > 0 && end > found) atomicMin(&refused, s);
     __syncthreads();
     const bool go = grow > 0 && s < refused;
-    const int served = refused < kThreads ? (refused > 0 ? end_of[refused - 1] : 0) : total;
-    int n_copies;
-    const int copy_at = block_scan(go && cow, &n_copies) - 1;
-    copies[s] = go && cow ? copy_at : -1;
+    const int64_t served = refused < kThreads ? (refused > 0 ? end_of[refused - 1] : 0) : total;
+    copies[s] = go && cow ? copies_to - 1 : -1;
+    if (s == (refused < kThreads ? refused : kThreads - 1)) ws[0] = copies_to - (refused < kThreads && cow ? 1 : 0);
     __syncthreads();
-    // free page number f (ascending) goes to the first sequence whose end is past f
-    int seen = 0;
+    // Free page number f (ascending) goes to the first sequence whose end is past f.
+    // A step's free pages go to a list first: they lie in runs, and a thread that
+    // searched for all sixteen of its own would keep the workgroup waiting.
+    int64_t seen = 0;
     for (int base = 0; base < c.n_pages && seen < served; base += kStep) {
         const int p = min(base + s * kPer, c.n_pages);
-        uint32_t m = free_mask(c, p);
-        int f = seen + block_scan(__popc(m), &got) - __popc(m);
-        for (; m && f < served; m &= m - 1, ++f) {
-            const int page = p + __ffs(m) - 1;
+        uint32_t m = base == 0 ? mask0 : free_mask(c, p);
+        const int pop = __popc(m);
+        int f = first0 - pop;
+        got = first_got;
+        if (base > 0) f = block_scan<int>(pop, &got) - pop;
+        for (; m; m &= m - 1, ++f) list[f] = p + __ffs(m) - 1;
+        __syncthreads();
+        const int take = (int)min((int64_t)got, served - seen);
+        for (int i = s; i < take; i += kThreads) {
+            const int page = list[i];
+            const int64_t at = seen + i;
             int lo = 0, hi = c.n_seqs - 1;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (end_of[mid] > f) hi = mid;
+                if (end_of[mid] > at) hi = mid;
                 else lo = mid + 1;
             }
-            const int k = f - (lo > 0 ? end_of[lo - 1] : 0);
+            const int k = (int)(at - (lo > 0 ? end_of[lo - 1] : 0));
             if (k == 0 && copies[lo] >= 0) ws[1 + c.n_seqs + copies[lo]] = page;
             c.table[(int64_t)lo * c.max_pages + place[lo] + k] = page;
             c.ref[page] = 1;
         }
+        __syncthreads();                           // the list is free again
         seen += got;
     }
     if (go && cow) {
-        ws[1 + copy_at] = last;
+        ws[1 + copies_to - 1] = last;
         atomicSub(c.ref + last, 1);
     }
-    if (s == 0) ws[0] = n_copies;
     if (s < c.n_seqs) {
         granted[s] = go ? grow : 0;
         if (go) c.len[s] = len + grow;
@@ -244,11 +271,12 @@ __global__ __launch_bounds__(kThreads) void kv4_compact_plan(Cache c, int32_t* _
                                                              int32_t* __restrict__ n_live, int32_t* __restrict__ ws) {
     const int t = threadIdx.x;
     int32_t *src = ws + 1, *dst = ws + 1 + c.n_pages / 2;
+    const uint32_t mask0 = free_mask(c, min(t * kPer, c.n_pages));
     int live = 0, got;
     for (int base = 0; base < c.n_pages; base += kStep) {
         const int p = min(base + t * kPer, c.n_pages);
         const int in = min(c.n_pages - p, kPer);
-        block_scan(in - __popc(free_mask(c, p)), &got);
+        block_scan<int>(in - __popc(base == 0 ? mask0 : free_mask(c, p)), &got);
         live += got;
     }
     int holes = 0, moves = 0;
@@ -256,12 +284,14 @@ __global__ __launch_bounds__(kThreads) void kv4_compact_plan(Cache c, int32_t* _
         const int p = min(base + t * kPer, c.n_pages);
         const int in = min(c.n_pages - p, kPer);
         const uint32_t all = (1u << in) - 1, below = p >= live ? 0 : live - p >= in ? all : (1u << (live - p)) - 1;
-        const uint32_t fr = free_mask(c, p);
+        const uint32_t fr = base == 0 ? mask0 : free_mask(c, p);
         uint32_t hole = fr & below, move = ~fr & all & ~below;
-        int h = holes + block_scan(__popc(hole), &got) - __popc(hole);
-        holes += got;
-        int v = moves + block_scan(__popc(move), &got) - __popc(move);
-        moves += got;
+        // both counts (at most 16384 a step) in one scan
+        const int both = block_scan<int>(__popc(hole) | __popc(move) << 16, &got);
+        int h = holes + (both & 0xFFFF) - __popc(hole);
+        holes += got & 0xFFFF;
+        int v = moves + (both >> 16) - __popc(move);
+        moves += got >> 16;
         for (int k = 0; k < in; ++k) {
             remap[p + k] = fr >> k & 1 ? -1 : p + k;
             if (hole >> k & 1) dst[h++] = p + k;

@@ -552,18 +552,21 @@ class KvCache:
         return self.data.device
 
     def struct(self) -> _KvCache:
-        dev, (L, P, nb), (S, mp) = self.device, self.data.shape, self.table.shape
+        data, table = self.data, self.table
+        dev, (L, P, nb), (S, mp) = data.device, data.shape, table.shape
         if dev.type != "cuda":
             raise ValueError("the cache must be on the GPU")
         if nb != self.kv_heads * self.page_tokens * (self.head_dim + 8):
             raise ValueError(f"data has {nb} bytes a page, expected kv_heads * page_tokens * (head_dim + 8)")
+        i32 = torch.int32
         return _KvCache(L, P, self.page_tokens, self.kv_heads, self.head_dim, S, mp,
-                        _on(self.data, torch.uint8, "data", dev, (L, P, nb)),
-                        _on(self.table, torch.int32, "table", dev, (S, mp)),
-                        _on(self.len, torch.int32, "len", dev, (S,)), _on(self.ref, torch.int32, "ref", dev, (P,)))
+                        _on(data, torch.uint8, "data", dev, data.shape), _on(table, i32, "table", dev, table.shape),
+                        _on(self.len, i32, "len", dev, (S,)), _on(self.ref, i32, "ref", dev, (P,)))
 
-    def _ints(self, t: torch.Tensor | None, name: str, n: int) -> int | None:
-        return None if t is None else _on(t, torch.int32, name, self.device, (n,))
+
+
+def _ints(t: torch.Tensor | None, name: str, dev: torch.device, n: int) -> int | None:
+    return None if t is None else _on(t, torch.int32, name, dev, (n,))
 
 
 def kv4_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
@@ -571,28 +574,28 @@ def kv4_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor, q_s
     """kv4_append: rows q_start[s] .. q_start[s+1]-1 of k and v [rows, kv_heads,
     head_dim] become the last positions of sequence s (len[s] already counts
     them; granted: what kv4_reserve gave)."""
-    c, dev, inner = cache.struct(), cache.device, (cache.kv_heads, cache.head_dim)
+    c, dev, inner = cache.struct(), cache.data.device, (cache.kv_heads, cache.head_dim)
     kp, ldk = _rows(k, inner, "k", dev)
     vp, ldv = _rows(v, inner, "v", dev)
     if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
         raise ValueError("k and v must have one dtype and as many rows")
     _launch("kv4_append", dev, ctypes.byref(c), layer, kp, ldk, vp, ldv, DTYPES[k.dtype], k.shape[0],
-            cache._ints(q_start, "q_start", cache.n_seqs + 1), cache._ints(granted, "granted", cache.n_seqs))
+            _ints(q_start, "q_start", dev, c.n_seqs + 1), _ints(granted, "granted", dev, c.n_seqs))
 
 
 def kv4_read(cache: KvCache, layer: int, first: torch.Tensor, q_start: torch.Tensor, rows: int,
              dtype: torch.dtype = torch.float32) -> tuple[torch.Tensor, torch.Tensor]:
     """kv4_read: the values of positions first[s] .. of sequence s in rows
     q_start[s] .. q_start[s+1]-1 of k and v [rows, kv_heads, head_dim]."""
-    c, dev = cache.struct(), cache.device
+    c, dev = cache.struct(), cache.data.device
     if dtype not in DTYPES:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     if rows < 0:
         raise ValueError("rows must not be negative")
     k, v = (torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev) for _ in range(2))
     ld = cache.kv_heads * cache.head_dim
-    _launch("kv4_read", dev, ctypes.byref(c), layer, cache._ints(first, "first", cache.n_seqs),
-            cache._ints(q_start, "q_start", cache.n_seqs + 1), rows, k.data_ptr(), ld, v.data_ptr(), ld,
+    _launch("kv4_read", dev, ctypes.byref(c), layer, _ints(first, "first", dev, c.n_seqs),
+            _ints(q_start, "q_start", dev, c.n_seqs + 1), rows, k.data_ptr(), ld, v.data_ptr(), ld,
             DTYPES[dtype])
     return k, v
 
@@ -606,7 +609,7 @@ def kv4_attention(q: torch.Tensor, cache: KvCache, layer: int, q_start: torch.Te
     0 keeps the last window keys of each query; max_len: an upper bound of the
     lengths, where the caller knows one (it sizes the launch only); lse: fp32
     [rows, heads] to fill with the log-sum-exp of the scores."""
-    c, dev = cache.struct(), cache.device
+    c, dev = cache.struct(), cache.data.device
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
     rows, heads = q.shape[0], q.shape[1]
@@ -617,12 +620,12 @@ def kv4_attention(q: torch.Tensor, cache: KvCache, layer: int, q_start: torch.Te
     if out.dtype != q.dtype or out.shape[0] != rows:
         raise ValueError("out must have q's dtype and rows")
     lp = None if lse is None else _on(lse, torch.float32, "lse", dev, (rows, heads))
-    cap = cache.max_pages * cache.page_tokens
+    cap = c.max_pages * c.page_tokens
     bound = cap if max_len is None else min(int(max_len), cap)
     nb = lib().kv4_attention_workspace(ctypes.byref(c), rows, heads, bound)
     ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb > 0 else None
     _launch("kv4_attention", dev, ctypes.byref(c), layer, qp, ldq, DTYPES[q.dtype], rows, heads,
-            cache._ints(q_start, "q_start", cache.n_seqs + 1), cache._ints(granted, "granted", cache.n_seqs),
+            _ints(q_start, "q_start", dev, c.n_seqs + 1), _ints(granted, "granted", dev, c.n_seqs),
             cache.head_dim ** -0.5 if scale is None else float(scale), window, bound, op, ldo, lp,
             ws.data_ptr() if nb > 0 else None, max(nb, 0))
     return out
@@ -632,10 +635,10 @@ def kv4_reserve(cache: KvCache, n_new: torch.Tensor) -> torch.Tensor:
     """kv4_reserve: len += n_new (int32 [n_seqs]) with pages for the new tokens,
     shared partly filled pages copied first; returns granted (n_new, or 0 where
     there was no room and nothing changed)."""
-    c, dev, S = cache.struct(), cache.device, cache.n_seqs
+    c, dev, S = cache.struct(), cache.data.device, cache.table.shape[0]
     granted = torch.empty(S, dtype=torch.int32, device=dev)
     ws = torch.empty(2 * S + 1, dtype=torch.int32, device=dev)
-    _launch("kv4_reserve", dev, ctypes.byref(c), cache._ints(n_new, "n_new", S), granted.data_ptr(), ws.data_ptr())
+    _launch("kv4_reserve", dev, ctypes.byref(c), _ints(n_new, "n_new", dev, S), granted.data_ptr(), ws.data_ptr())
     return granted
 
 
@@ -643,24 +646,24 @@ def kv4_fork(cache: KvCache, src: torch.Tensor, dst: torch.Tensor,
              n_tokens: torch.Tensor | None = None) -> torch.Tensor:
     """kv4_fork: the empty slots dst[i] become branches of src[i] (its first
     n_tokens[i] tokens) that share its pages; returns ok (int32, 1 or 0)."""
-    c, dev, n = cache.struct(), cache.device, src.shape[0]
+    c, dev, n = cache.struct(), cache.data.device, src.shape[0]
     ok = torch.empty(n, dtype=torch.int32, device=dev)
-    _launch("kv4_fork", dev, ctypes.byref(c), n, cache._ints(src, "src", n), cache._ints(dst, "dst", n),
-            cache._ints(n_tokens, "n_tokens", n), ok.data_ptr())
+    _launch("kv4_fork", dev, ctypes.byref(c), n, _ints(src, "src", dev, n), _ints(dst, "dst", dev, n),
+            _ints(n_tokens, "n_tokens", dev, n), ok.data_ptr())
     return ok
 
 
 def kv4_truncate(cache: KvCache, new_len: torch.Tensor) -> None:
     """kv4_truncate: sequence s keeps its first new_len[s] tokens (negative:
     untouched, 0: freed); pages nothing holds any more become free."""
-    c = cache.struct()
-    _launch("kv4_truncate", cache.device, ctypes.byref(c), cache._ints(new_len, "new_len", cache.n_seqs))
+    c, dev = cache.struct(), cache.data.device
+    _launch("kv4_truncate", dev, ctypes.byref(c), _ints(new_len, "new_len", dev, c.n_seqs))
 
 
 def kv4_compact(cache: KvCache) -> tuple[torch.Tensor, torch.Tensor]:
     """kv4_compact: live pages move to the front of the pool; returns (remap
     int32 [n_pages]: new index of every page or -1, n_live int32 [1])."""
-    c, dev, P = cache.struct(), cache.device, cache.n_pages
+    c, dev, P = cache.struct(), cache.data.device, cache.data.shape[1]
     remap = torch.empty(P, dtype=torch.int32, device=dev)
     live = torch.empty(1, dtype=torch.int32, device=dev)
     ws = torch.empty(P + 1, dtype=torch.int32, device=dev)
