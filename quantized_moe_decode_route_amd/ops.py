@@ -808,9 +808,49 @@ def moe_layer(x: torch.Tensor, router_w: torch.Tensor, bias: torch.Tensor, ex: E
     return buf
 
 
+@dataclass
+class Attention:
+    """One layer's attention on packed weights: a fused query/key/value projection
+    and the output projection."""
+    qkv: Linear            # [(heads + 2 * kv_heads) * head_dim, hidden]: queries, then keys, then values
+    out: Linear            # [hidden, heads * head_dim]
+    heads: int
+    scale: float | None = None   # of the scores; None: head_dim^-0.5
+    window: int = 0              # > 0: keys each query sees at most
+    rotate: object = None        # callable(q, k): position encoding, in place on views [T, heads, head_dim]
+
+
+def attention_block(x: torch.Tensor, at: Attention, cache: KvCache, layer: int, q_start: torch.Tensor, *,
+                    granted: torch.Tensor | None = None, max_len: int | None = None, eps: float = 1e-6,
+                    xn: torch.Tensor | None = None) -> None:
+    """x <- x + W_o attention(W_qkv rmsnorm(x)), in place on x (fp32 [T, hidden]):
+    the tokens' keys and values go to the cache (positions as for kv4_append, so
+    kv4_reserve first), then every token attends.  xn: a scratch like x."""
+    T, D, Hk = x.shape[0], cache.head_dim, cache.kv_heads
+    nq, nk = at.heads * D, Hk * D
+    if at.qkv.n_out != nq + 2 * nk or at.out.n_in != nq or at.out.n_out != x.shape[1]:
+        raise ValueError("qkv must have (heads + 2 * kv_heads) * head_dim rows, out be [hidden, heads * head_dim]")
+    if xn is None:
+        xn = torch.empty_like(x)
+    residual_rmsnorm(x, None, xn, eps)
+    qkv = linear(xn, at.qkv)
+    q = qkv[:, :nq].unflatten(1, (at.heads, D))
+    k = qkv[:, nq:nq + nk].unflatten(1, (Hk, D))
+    v = qkv[:, nq + nk:].unflatten(1, (Hk, D))
+    if at.rotate is not None:
+        at.rotate(q, k)
+    kv4_append(cache, layer, k, v, q_start, granted)
+    # rows of no sequence (padding) attend to nothing: zeros, not what the memory held
+    o = torch.zeros((T, at.heads, D), dtype=x.dtype, device=x.device)
+    kv4_attention(q, cache, layer, q_start, scale=at.scale, window=at.window, granted=granted, max_len=max_len, out=o)
+    linear(o.view(T, nq), at.out, residual=x, out=x)
+
+
 def stack_forward(x: torch.Tensor, layers: list, bufs: list, *, n_group: int, topk_group: int, top_k: int,
                   rsf: float, eps: float = 1e-6, top_p: float | None = None, fused: bool | None = None,
-                  xn: torch.Tensor | None = None, check: bool | None = None) -> bool:
+                  xn: torch.Tensor | None = None, check: bool | None = None, attn: list | None = None,
+                  cache: KvCache | None = None, q_start: torch.Tensor | None = None,
+                  granted: torch.Tensor | None = None, max_len: int | None = None) -> bool:
     """x <- x + MoE_l(rmsnorm(x)) for every layer l, in place on x (the
     pre-norm residual stack).  layers[l] = (router_w, bias, Experts); bufs[l]
     a LayerBuffers.  Fused: one moe_layer_fused_resid launch per layer (the
@@ -818,6 +858,11 @@ def stack_forward(x: torch.Tensor, layers: list, bufs: list, *, n_group: int, to
     moe_residual_rmsnorm between them (xn: a [T, H] scratch for the normalised
     tokens).  fused=None tries the fused form on the first layer and keeps
     whichever runs; returns whether the fused form ran.
+
+    attn[l] (an Attention each) puts x <- x + Attn_l(rmsnorm(x)) before layer l's
+    experts: whole decoder layers.  The tokens are the newest positions of their
+    sequences in cache (kv4_reserve first; q_start, granted, max_len as for
+    kv4_append and kv4_attention; cache layer l belongs to layer l).
 
     A fused layer whose grid-wide wait timed out writes an invalid x for every
     later layer; check=True (or None outside graph capture) synchronises once
@@ -827,12 +872,37 @@ def stack_forward(x: torch.Tensor, layers: list, bufs: list, *, n_group: int, to
     kw = dict(n_group=n_group, topk_group=topk_group, top_k=top_k, rsf=rsf)
     if check is None:
         check = not torch.cuda.is_current_stream_capturing()
+    if attn is not None:
+        if cache is None or q_start is None or len(attn) != len(layers) or cache.layers < len(layers):
+            raise ValueError("attn takes one Attention per layer, a cache with as many layers, and q_start")
+        if xn is None:
+            xn = torch.empty_like(x)
 
-    def run_fused(items) -> None:
-        for (rw, b, ex), buf in items:
-            layer_fused(x, rw, b, ex, buf=buf, top_p=top_p, x_out=x, eps=eps, check=False, **kw)
+    def attend(l: int) -> None:
+        if attn is not None:
+            attention_block(x, attn[l], cache, l, q_start, granted=granted, max_len=max_len, eps=eps, xn=xn)
 
-    def finish() -> bool:
+    def run_fused(l: int) -> None:
+        rw, b, ex = layers[l]
+        layer_fused(x, rw, b, ex, buf=bufs[l], top_p=top_p, x_out=x, eps=eps, check=False, **kw)
+
+    done = 0                               # layers whose attention has run
+    if fused is None:
+        fused = fused_supported(T, layers[0][2])
+        if fused:
+            attend(0)
+            done = 1
+            try:
+                run_fused(0)
+            except MoedecError as err:
+                if err.status != MOEDEC_ERR_UNSUPPORTED:
+                    raise
+                fused = False
+    if fused:
+        for l in range(min(len(layers), len(bufs))):
+            if l >= done:
+                attend(l)
+                run_fused(l)
         if check:
             bad = [buf for buf in bufs if buf.fused_error()]
             for buf in bad:
@@ -841,26 +911,15 @@ def stack_forward(x: torch.Tensor, layers: list, bufs: list, *, n_group: int, to
                 raise MoedecError("moe_layer_fused_resid", MOEDEC_ERR_DEVICE,
                                   f"{len(bad)} layer(s) timed out in a grid-wide wait; x is invalid")
         return True
-
-    if fused is None:
-        fused = fused_supported(T, layers[0][2])
-        if fused:
-            try:
-                run_fused(list(zip(layers, bufs))[:1])
-            except MoedecError as err:
-                if err.status != MOEDEC_ERR_UNSUPPORTED:
-                    raise
-                fused = False
-            else:
-                run_fused(list(zip(layers, bufs))[1:])
-                return finish()
-    if fused:
-        run_fused(list(zip(layers, bufs)))
-        return finish()
     if xn is None:
         xn = torch.empty_like(x)
-    residual_rmsnorm(x, None, xn, eps)
-    for (rw, b, ex), buf in zip(layers, bufs):
+    if attn is None:
+        residual_rmsnorm(x, None, xn, eps)
+    for l, ((rw, b, ex), buf) in enumerate(zip(layers, bufs)):
+        if attn is not None:
+            if l >= done:
+                attend(l)
+            residual_rmsnorm(x, None, xn, eps)
         moe_layer(xn, rw, b, ex, buf=buf, fused=False, top_p=top_p, **kw)
         residual_rmsnorm(x, buf.y, xn, eps)
     return False
