@@ -73,27 +73,36 @@ __device__ __forceinline__ Params load_params(const LinearArgs& a, int r) {
     return p;
 }
 
-// The epilogue of rows r .. r+3 of token t; `whole`: y is aligned for one store
-// of four outputs.
+// Four consecutive elements at any element's alignment (one load or store: the
+// memory system takes them from any address).
+template <typename T>
+struct Four {
+    typedef typename T::type type __attribute__((ext_vector_type(4), aligned(T::bytes)));
+};
+
+// The epilogue of rows r .. r+3 of token t.
 template <typename T>
 __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int r, float inv, const floatx4& sum,
-                                        const Params& p, bool whole) {
+                                        const Params& p) {
     if (r >= a.N) return;
+    typedef typename Four<T>::type four;
     typename T::type* y = reinterpret_cast<typename T::type*>(a.y) + (int64_t)t * a.ldy + r;
     const typename T::type* res = reinterpret_cast<const typename T::type*>(a.residual) + (int64_t)t * a.ldr + r;
+    const bool whole = r + 3 < a.N;
+    four old = {};
+    if (a.residual && whole) old = *reinterpret_cast<const four*>(res);
     float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = sum[i] * inv * p.scale[i];
-        if (a.bias) v[i] += p.bias[i];
-        v[i] = activate(v[i], a.act);
-    }
-    if (whole && r + 3 < a.N) {
-        if (a.residual) {
+    for (int i = 0; i < 4; ++i) v[i] = sum[i] * inv * p.scale[i] + p.bias[i];
+    if (a.act != MOEDEC_ACT_NONE) {                // uniform
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += T::get(res[i]);
-        }
-        store4<T>(y, v);
+        for (int i = 0; i < 4; ++i) v[i] = activate(v[i], a.act);
+    }
+    if (whole) {
+        four o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = T::put(a.residual ? v[i] + T::get(old[i]) : v[i]);
+        *reinterpret_cast<four*>(y) = o;
         return;
     }
 #pragma unroll
@@ -296,7 +305,7 @@ template <typename T, int BITS, int NB, int TB, int WN, int WT, int D>
 __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, const half8* __restrict__ hi,
                                                                const half8* __restrict__ lo,
                                                                const float* __restrict__ inv, float* __restrict__ part,
-                                                               int calls, int splits, bool whole) {
+                                                               int calls, int splits) {
     constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
     constexpr int kW = WN * WT;
     constexpr int kLoads = WT * TB * kStage / kW;          // 1 KB direct loads a wave makes per step
@@ -416,7 +425,7 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             const int tok = (tb0 + wt * TB + t) * 16 + n;
-            if (tok < a.T) finish4<T>(a, tok, r, inv[tok], acc[b][t], par, whole);
+            if (tok < a.T) finish4<T>(a, tok, r, inv[tok], acc[b][t], par);
         }
     }
 }
@@ -425,7 +434,7 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
 constexpr int kJoinThreads = 256;
 template <typename T>
 __global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const float* __restrict__ inv,
-                                                            const float* __restrict__ part, int splits, bool whole) {
+                                                            const float* __restrict__ part, int splits) {
     const int quads = (a.N + 3) / 4, blocks = (quads + kJoinThreads - 1) / kJoinThreads;
     const int t = blockIdx.x / blocks, r = (blockIdx.x % blocks * kJoinThreads + threadIdx.x) * 4;
     if (r >= a.N) return;
@@ -434,7 +443,7 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const 
     floatx4 v = p[0];
 #pragma unroll 4
     for (int s = 1; s < splits; ++s) v += p[(int64_t)s * a.T * quads];
-    finish4<T>(a, t, r, inv[t], v, par, whole);
+    finish4<T>(a, t, r, inv[t], v, par);
 }
 
 // ------------------------------------------------------------- some tokens
@@ -449,7 +458,7 @@ constexpr int kRowFlight = 4;               // even: the operands' two buffers a
 template <typename T, int BITS, int TB, int NB>
 __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, const half8* __restrict__ hi,
                                                                  const half8* __restrict__ lo,
-                                                                 const float* __restrict__ inv, int calls, bool whole) {
+                                                                 const float* __restrict__ inv, int calls) {
     using M = MfmaCodec<BITS>;
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
@@ -523,7 +532,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
 #pragma unroll
     for (int w = 1; w < kRowWaves; ++w) v += part[w][wave][lane];
     const int tok = ft * 16 + n;
-    if (tok < a.T) finish4<T>(a, tok, r0 + 16 * fb + 4 * g, inv[tok], v, par, whole);
+    if (tok < a.T) finish4<T>(a, tok, r0 + 16 * fb + 4 * g, inv[tok], v, par);
 }
 
 // -------------------------------------------------------------- few tokens
@@ -539,7 +548,7 @@ constexpr int kFewFlight = 8;             // chunks a wave has in flight
 constexpr int kFewUnits = 8;              // units a thread converts at most
 
 template <typename T, int BITS>
-__global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, int calls, bool whole) {
+__global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, int calls) {
     using M = MfmaCodec<BITS>;
     constexpr int CW = 128 / BITS;
     constexpr int kThreads = kRowWaves * kWave;
@@ -627,7 +636,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
         for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor(sum[i], 8, kWave);
     }
     if (tok >= a.T || (kPlanes == 2 && n >= 8)) return;
-    finish4<T>(a, tok, r0 + 4 * g, pow2(-row_exponent(__uint_as_float(top[tok]))), sum, par, whole);
+    finish4<T>(a, tok, r0 + 4 * g, pow2(-row_exponent(__uint_as_float(top[tok]))), sum, par);
 }
 
 // ------------------------------------------------------------------- launches
@@ -640,33 +649,36 @@ bool few(int64_t T, int64_t K, int bits, int bytes) {
     return T <= kFewTokens && n * (bytes == 4 ? 4 : 2) <= kFewLds && n / 8 <= kFewUnits * kRowWaves * kWave;
 }
 
-// One store of four outputs is possible.
-bool whole4(const LinearArgs& a, int bytes) {
-    const uintptr_t m = 4 * bytes - 1;
-    return !(reinterpret_cast<uintptr_t>(a.y) & m) && !(a.ldy * bytes & m);
-}
-
-// The tile of linear_gemm (weight rows by tokens) and the parts of K.
+// The tile of linear_gemm and the parts of K.  Two tiles: 128 weight rows by 64
+// tokens, of which a compute unit holds two (sixteen waves hide the loads of short
+// runs), and 256 by 256, one a compute unit, 1.3 times as fast per output where
+// there are enough of them.  Up to 512 small tiles K is split until the compute
+// units have one or two each (at least 512 columns a part); beyond that the two
+// are priced by the rounds they take, 2.8 fs for an output's column in a small
+// tile's round, and the joining of the parts at 5 TB/s.  Measured at 6144 -> 8192
+// in int4, bf16: 64 tokens 24 us small against 47 large, 256: 50 / 59, 512: 79 /
+// 84, 1024: 160 / 149, 4096: - / 449.
 struct Tiling {
-    int rows, tokens, splits;
+    bool large;
+    int splits;
 };
-Tiling tiling(int64_t T, int64_t K, int64_t N, int bits) {
+Tiling tiling(int64_t T, int64_t K, int64_t N, int bits, int bytes) {
     auto count = [&](int r, int t) { return ((N + r - 1) / r) * ((T + t - 1) / t); };
-    // the largest tile that still gives most compute units a workgroup; below
-    // that, K is split until they have one, at least 4 steps of 128 columns each
-    Tiling k;
-    if (count(256, 256) >= 200) k = {256, 256, 1};
-    else if (T > 64) k = {128, 128, 1};
-    else k = {128, 64, 1};
-    if (k.rows == 128) {
-        const int64_t tiles = count(k.rows, k.tokens), most = padded(K, bits) / 512;
-        // (two for the 128-token tile, whose workgroups are half as large)
-        const int64_t want = k.tokens == 128 ? 2 * kCus : kCus;
+    const int64_t small = count(128, 64), most = padded(K, bits) / 512;
+    auto parts = [&](int64_t tiles, int64_t want) {
         int64_t s = (want + tiles / 2) / tiles;
         if (s > most) s = most;
-        k.splits = (int)(s < 1 ? 1 : s > 16 ? 16 : s);
-    }
-    return k;
+        return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+    };
+    if (small <= 2 * kCus) return {false, parts(small, small < kCus / 2 ? kCus : 2 * kCus)};
+    const int64_t large = count(256, 256);
+    const int s = parts(large, kCus);
+    const double unit = 2.8e-9 * (double)K * (bytes == 4 ? 2 : 1);                          // us an output
+    const double t_small = unit * 128 * 64 * 2 * kCus * ((small + 2 * kCus - 1) / (2 * kCus));
+    const double t_large = unit * 256 * 256 * kCus / (1.3 * s) * ((large * s + kCus - 1) / kCus) +
+                           (s > 1 ? 3.0 + 1.6e-6 * s * (double)T * N : 0.0);
+    if (t_small <= t_large) return {false, 1};
+    return {true, s};
 }
 
 template <typename T, int BITS, int NB, int TB, int WN, int WT, int D>
@@ -675,11 +687,11 @@ void launch_gemm(const LinearArgs& a, const half8* hi, const half8* lo, const fl
     const int64_t tiles = (int64_t)((a.N + WN * NB * 16 - 1) / (WN * NB * 16)) *
                           ((a.T + WT * TB * 16 - 1) / (WT * TB * 16)) * splits;
     hipLaunchKernelGGL((linear_gemm<T, BITS, NB, TB, WN, WT, D>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                       dim3(WN * WT * kWave), 0, st, a, hi, lo, inv, part, calls, splits, whole4(a, T::bytes));
+                       dim3(WN * WT * kWave), 0, st, a, hi, lo, inv, part, calls, splits);
     if (splits > 1) {
         const int64_t blocks = ((a.N + 3) / 4 + kJoinThreads - 1) / kJoinThreads;
         hipLaunchKernelGGL((linear_join<T>), dim3((unsigned)(blocks * a.T)), dim3(kJoinThreads), 0, st, a, inv, part,
-                           splits, whole4(a, T::bytes));
+                           splits);
     }
 }
 
@@ -708,14 +720,13 @@ void launch_prepare(const LinearArgs& a, half8* hi, half8* lo, float* inv, int c
 
 template <typename T, int BITS, int TB>
 void launch_rows(const LinearArgs& a, const half8* hi, const half8* lo, const float* inv, int calls, hipStream_t st) {
-    const bool whole = whole4(a, T::bytes);
     // two row blocks a workgroup where that still gives every compute unit one
     if (a.N >= kCus * 32)
         hipLaunchKernelGGL((linear_rows<T, BITS, TB, 2>), dim3((a.N + 31) / 32), dim3(kRowWaves * kWave), 0, st, a, hi,
-                           lo, inv, calls, whole);
+                           lo, inv, calls);
     else
         hipLaunchKernelGGL((linear_rows<T, BITS, TB, 1>), dim3((a.N + 15) / 16), dim3(kRowWaves * kWave), 0, st, a, hi,
-                           lo, inv, calls, whole);
+                           lo, inv, calls);
 }
 
 template <typename T, int BITS>
@@ -724,8 +735,7 @@ hipError_t launch_bits(const LinearArgs& a, hipStream_t st) {
     const int calls = (int)(Kp / 32);
     if (few(a.T, a.K, BITS, T::bytes)) {
         const size_t lds = (size_t)a.T * Kp * (T::bytes == 4 ? 4 : 2);
-        hipLaunchKernelGGL((linear_few<T, BITS>), dim3((a.N + 15) / 16), dim3(kRowWaves * kWave), lds, st, a, calls,
-                           whole4(a, T::bytes));
+        hipLaunchKernelGGL((linear_few<T, BITS>), dim3((a.N + 15) / 16), dim3(kRowWaves * kWave), lds, st, a, calls);
         return hipGetLastError();
     }
     const int64_t blocks = blocks16(a.T);
@@ -739,9 +749,8 @@ hipError_t launch_bits(const LinearArgs& a, hipStream_t st) {
     } else if (a.T <= kRowsTokens) {
         launch_rows<T, BITS, 2>(a, hi, lo, inv, calls, st);
     } else {
-        const Tiling k = tiling(a.T, a.K, a.N, BITS);
-        if (k.rows == 256) launch_gemm<T, BITS, 4, 8, 4, 2, 2>(a, hi, lo, inv, part, calls, k.splits, st);
-        else if (k.tokens == 128) launch_gemm<T, BITS, 4, 4, 2, 2, 2>(a, hi, lo, inv, part, calls, k.splits, st);
+        const Tiling k = tiling(a.T, a.K, a.N, BITS, T::bytes);
+        if (k.large) launch_gemm<T, BITS, 4, 8, 4, 2, 2>(a, hi, lo, inv, part, calls, k.splits, st);
         else launch_gemm<T, BITS, 1, 4, 8, 1, 4>(a, hi, lo, inv, part, calls, k.splits, st);
     }
     return hipGetLastError();
@@ -764,7 +773,7 @@ int64_t linear_workspace(int bits, int dtype, int64_t T, int64_t K, int64_t N) {
     if (T == 0 || few(T, K, bits, bytes)) return 0;
     int64_t n = blocks16(T) * 16 * (padded(K, bits) * bytes + 4);
     if (T > kRowsTokens) {
-        const int splits = tiling(T, K, N, bits).splits;
+        const int splits = tiling(T, K, N, bits, bytes).splits;
         if (splits > 1) n += splits * T * ((N + 3) / 4 * 16);
     }
     return n;
