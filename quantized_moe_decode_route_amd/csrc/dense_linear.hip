@@ -1,12 +1,24 @@
 // y = act(scale * (x . codes) + bias) + residual on packed row-scaled weights.
 //
-// The codes are exact in fp16 and so, up to the exponent range, is every fp16 or
-// bf16 activation once its row is scaled by a power of two that brings the
-// largest magnitude to [2^14, 2^15): the products on v_mfma_f32_16x16x32_f16 are
-// then exact and only the fp32 sums round.  fp32 activations enter as a hi/lo
-// pair of fp16 (about 22 bits), two MFMAs instead of one.  The power of two, the
-// row scale, bias, activation and residual are applied once, in fp32, to the
-// sums.
+// Codes.  A code q of b bits may enter as the unsigned u = q + 2^(b-1), isolated
+// with its sign bit flipped by one bit operation and left where it stands in the
+// low byte of its 16-bit half: read as fp16 that is the subnormal u * 2^j * 2^-24,
+// j its bit position, exactly.  The 2^j is taken out of the activation that meets
+// it, 2^24 out of the sum, and the offset out of the start of the sum,
+//   sum x q = -2^(b-1) sum x + sum x u,
+// with sum x over the activations as they enter.  Converting 8 codes of 4 bits then
+// costs 5 vector instructions instead of 9, of 8 bits 6 instead of 10, of 2 bits
+// 4.5 instead of 12; but the terms are about four times as large for 4 and 8 bits
+// (1.5 times for 2), and the fp32 rounding of the sum with them.  That disappears
+// in a 16-bit result; fp32 results keep signed codes at 4 and 8 bits.  (int4, bf16,
+// 6144 -> 8192: 1024 tokens 136 us, 146 with signed codes, 4096 tokens 426 / 449.)
+//
+// Activations.  Every fp16 or bf16 activation is exact in fp16, up to the exponent
+// range, once its row is scaled by a power of two that brings the largest
+// magnitude to [2^14, 2^15): the products on v_mfma_f32_16x16x32_f16 are then
+// exact and only the fp32 sums round.  fp32 activations enter as a hi/lo pair of
+// fp16 (about 22 bits), two MFMAs instead of one.  The power of two, the row scale,
+// bias, activation and residual are applied once, in fp32, to the sums.
 //
 // Weight rows are the M side (A operand: lane l holds row l % 16), tokens the N
 // side.  A wave turns the packed codes into fp16 in its own registers: at 2 to 8
@@ -22,10 +34,52 @@ namespace {
 
 using mfma::MfmaCodec;
 
-template <int BITS>
+// Codes of a 32-bit word as unsigned fields in fp16 subnormals (see above): the
+// fields `mask` selects of both halves, their sign bits `flip` inverted.
+__device__ __forceinline__ uint32_t fields(uint32_t w, uint32_t mask, uint32_t flip) { return (w & mask) ^ flip; }
+
+// Whether codes enter as unsigned fields, for elements of that many bytes.
+constexpr bool offset_codes(int bits, int bytes) { return bits == 2 || bytes == 2; }
+
+// Operand of call c of a 16-byte group of codes, in the element order of
+// MfmaCodec: element e holds u * 2^field_bit(e) * 2^-24 (kOffset) or q.
+template <int BITS, bool kOffset>
 __device__ __forceinline__ half8 a_operand(const uint4& q, int c) {
-    if constexpr (BITS == 4) return codes_f16(mfma::dword(q, c));
-    else return mfma::a_operand<BITS>(q, c);
+    if constexpr (!kOffset) {
+        if constexpr (BITS == 4) return codes_f16(mfma::dword(q, c));
+        else return mfma::a_operand<BITS>(q, c);
+    }
+    u32x4 p;
+    if constexpr (BITS == 4) {
+        const uint32_t w = mfma::dword(q, c), h = w >> 8;
+        p = u32x4{fields(w, 0x000F000Fu, 0x00080008u), fields(w, 0x00F000F0u, 0x00800080u),
+                  fields(h, 0x000F000Fu, 0x00080008u), fields(h, 0x00F000F0u, 0x00800080u)};
+    } else if constexpr (BITS == 8) {
+        const uint32_t w0 = mfma::dword(q, 2 * c), w1 = mfma::dword(q, 2 * c + 1);
+        p = u32x4{fields(w0, 0x00FF00FFu, 0x00800080u), fields(w0 >> 8, 0x00FF00FFu, 0x00800080u),
+                  fields(w1, 0x00FF00FFu, 0x00800080u), fields(w1 >> 8, 0x00FF00FFu, 0x00800080u)};
+    } else {
+        const uint32_t w = mfma::dword(q, c >> 1) >> (8 * (c & 1));
+        p = u32x4{fields(w, 0x00030003u, 0x00020002u), fields(w, 0x000C000Cu, 0x00080008u),
+                  fields(w, 0x00300030u, 0x00200020u), fields(w, 0x00C000C0u, 0x00800080u)};
+    }
+    return __builtin_bit_cast(half8, p);
+}
+// Bit position of element e's field in its half.
+template <int BITS, bool kOffset>
+__device__ __forceinline__ constexpr int field_bit(int e) {
+    return !kOffset ? 0 : BITS == 4 ? 4 * ((e >> 1) & 1) : BITS == 2 ? 2 * (e >> 1) : 0;
+}
+// The offset as an operand: u = -2^(BITS-1) in every element.
+template <int BITS>
+__device__ __forceinline__ half8 minus_offset() {
+    constexpr uint32_t sign = 0x80008000u;
+    u32x4 p;
+    if constexpr (BITS == 4) p = u32x4{0x00080008u | sign, 0x00800080u | sign, 0x00080008u | sign, 0x00800080u | sign};
+    else if constexpr (BITS == 8)
+        p = u32x4{0x00800080u | sign, 0x00800080u | sign, 0x00800080u | sign, 0x00800080u | sign};
+    else p = u32x4{0x00020002u | sign, 0x00080008u | sign, 0x00200020u | sign, 0x00800080u | sign};
+    return __builtin_bit_cast(half8, p);
 }
 
 constexpr int kPrepThreads = 256;
@@ -81,7 +135,7 @@ struct Four {
 };
 
 // The epilogue of rows r .. r+3 of token t.
-template <typename T>
+template <typename T, bool kOffset>
 __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int r, float inv, const floatx4& sum,
                                         const Params& p) {
     if (r >= a.N) return;
@@ -93,7 +147,7 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int r, float
     if (a.residual && whole) old = *reinterpret_cast<const four*>(res);
     float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = sum[i] * inv * p.scale[i] + p.bias[i];
+    for (int i = 0; i < 4; ++i) v[i] = sum[i] * (kOffset ? 0x1p24f : 1.f) * inv * p.scale[i] + p.bias[i];
     if (a.act != MOEDEC_ACT_NONE) {                // uniform
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = activate(v[i], a.act);
@@ -158,14 +212,23 @@ template <int BITS>
 __device__ __forceinline__ constexpr int unit_element(int e) {
     return BITS == 8 ? 4 * (e >> 2) + ((e >> 1) & 1) + 2 * (e & 1) : (e >> 1) + 4 * (e & 1);
 }
-template <int BITS>
+// The unit's operands: element e times f * 2^-field_bit(e), as a pair.
+template <int BITS, bool kOffset>
 __device__ __forceinline__ void split_unit(const float* v, float f, half8& hi, half8& lo) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const mfma::F16Pair p = mfma::split_f16(v[unit_element<BITS>(e)], f);
+        const mfma::F16Pair p = mfma::split_f16(v[unit_element<BITS>(e)], f * (1.0f / (1 << field_bit<BITS, kOffset>(e))));
         hi[e] = p.hi;
         lo[e] = p.lo;
     }
+}
+// The sum of a unit's operands, their field positions taken out.
+template <int BITS, bool kPair>
+__device__ __forceinline__ float unit_sum(const half8& hi, const half8& lo) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += ((float)hi[e] + (kPair ? (float)lo[e] : 0.f)) * (float)(1 << field_bit<BITS, true>(e));
+    return s;
 }
 
 __device__ __forceinline__ float max8(const float* v, float m) {
@@ -186,13 +249,19 @@ __device__ __forceinline__ float max8(const float* v, float m) {
 // twice).  HBM-bound for many tokens (x read once, the planes written once; the 16
 // bytes a lane stores meet those of the block's other tokens in the L2 of one
 // XCD), a few microseconds of latency for few: those take four waves a token.
+struct Row {
+    float inv;                           // 1 / the row's power of two
+    float start;                         // of the sum: -2^(BITS-1) * 2^-24 times the sum of the row, or 0
+};
+
 template <typename T, int BITS, int NU, int WPT>
 __global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T::type* __restrict__ x, int64_t ldx,
                                                                int T_, int K, int calls, half8* __restrict__ hi,
-                                                               half8* __restrict__ lo, float* __restrict__ inv) {
+                                                               half8* __restrict__ lo, Row* __restrict__ info) {
     constexpr int kPer = kPrepThreads / kWave / WPT;       // tokens of a workgroup
     constexpr int kParts = 16 / kPer;                      // workgroups of a block of 16 tokens: all on one XCD
     constexpr int kLanes = WPT * kWave;
+    constexpr bool kOffset = offset_codes(BITS, T::bytes);
     __shared__ float red[kPrepThreads / kWave];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), j = threadIdx.x % kLanes;
     const int xcd = blockIdx.x % 8, i8 = blockIdx.x / 8;
@@ -203,9 +272,11 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T:
     const bool on = t < T_;
     const typename T::type* row = x + (on ? t : 0) * ldx;
     const int units = calls * 4, cols = on ? K : 0;
+    float sum = 0.f;
     auto put = [&](int u, const float* v, float f) {
         half8 h, l;
-        split_unit<BITS>(v, f, h, l);
+        split_unit<BITS, kOffset>(v, f, h, l);
+        if (kOffset) sum += unit_sum<BITS, T::bytes == 4>(h, l);
         const int64_t at = (block * calls + (u >> 2)) * kWave + (u & 3) * 16 + n;
         hi[at] = h;
         if (T::bytes == 4) lo[at] = l;
@@ -242,7 +313,19 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T:
             put(u, v, f);
         }
     }
-    if (j == 0) inv[t] = pow2(-row_exponent(m));
+    if (kOffset) sum = group_sum<kWave>(sum);
+    if constexpr (WPT > 1 && kOffset) {
+        __syncthreads();                                   // the maxima are read
+        if ((threadIdx.x & (kWave - 1)) == 0) red[wave] = sum;
+        __syncthreads();
+        sum = (red[0] + red[1]) + (red[2] + red[3]);
+    }
+    if (j == 0) {
+        Row r;
+        r.inv = pow2(-row_exponent(m));
+        r.start = kOffset ? sum * (-(float)(1 << (BITS - 1)) * 0x1p-24f) : 0.f;
+        info[t] = r;
+    }
 }
 
 // ------------------------------------------------------------- many tokens
@@ -274,13 +357,13 @@ __device__ __forceinline__ Packed<BITS> load_packed(const uint8_t* tile, uint32_
     return p;
 }
 // The A operand of call c (0 .. 3) of a packed step.
-template <int BITS>
+template <int BITS, bool kOffset>
 __device__ __forceinline__ half8 step_operand(const Packed<BITS>& p, int c) {
-    if constexpr (BITS == 4) return a_operand<4>(uint4{p.w[0], p.w[1], p.w[2], p.w[3]}, c);
+    if constexpr (BITS == 4) return a_operand<4, kOffset>(uint4{p.w[0], p.w[1], p.w[2], p.w[3]}, c);
     else if constexpr (BITS == 8)
-        return a_operand<8>(uint4{p.w[4 * (c >> 1)], p.w[4 * (c >> 1) + 1], p.w[4 * (c >> 1) + 2],
+        return a_operand<8, kOffset>(uint4{p.w[4 * (c >> 1)], p.w[4 * (c >> 1) + 1], p.w[4 * (c >> 1) + 2],
                                   p.w[4 * (c >> 1) + 3]}, c & 1);
-    else return a_operand<2>(uint4{p.w[0], p.w[1], 0, 0}, c);
+    else return a_operand<2, kOffset>(uint4{p.w[0], p.w[1], 0, 0}, c);
 }
 
 // Workgroup tile: WN * NB * 16 weight rows by WT * TB * 16 tokens, WN x WT waves,
@@ -304,7 +387,7 @@ __device__ __forceinline__ void wait_loads_and_barrier() {
 template <typename T, int BITS, int NB, int TB, int WN, int WT, int D>
 __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, const half8* __restrict__ hi,
                                                                const half8* __restrict__ lo,
-                                                               const float* __restrict__ inv, float* __restrict__ part,
+                                                               const Row* __restrict__ info, float* __restrict__ part,
                                                                int calls, int splits) {
     constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
     constexpr int kW = WN * WT;
@@ -345,10 +428,13 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
     };
 
     floatx4 acc[NB][TB];
+    // tokens past the end belong to the last block's padding or repeat it: any start will do
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int t = 0; t < TB; ++t) {
+        const float s = split == 0 ? info[min((tb0 + wt * TB + t), last_tb) * 16 + n].start : 0.f;
 #pragma unroll
-        for (int t = 0; t < TB; ++t) acc[b][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < NB; ++b) acc[b][t] = floatx4{s, s, s, s};
+    }
     // Packed steps held.  One plane: the ring follows the buffers (with one step
     // ahead the loop is not unrolled and the next codes move over: unrolled by two
     // it spilled registers).  Two planes: a packed step lasts two steps, the next
@@ -396,7 +482,7 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
                 half8 w[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    w[b] = step_operand<BITS>(pk[kMove ? 0 : kPlanes == 2 ? j / 2 : j % kPackRing][b], kPlanes == 2 ? 2 * (j % 2) + c : c);
+                    w[b] = step_operand<BITS, offset_codes(BITS, T::bytes)>(pk[kMove ? 0 : kPlanes == 2 ? j / 2 : j % kPackRing][b], kPlanes == 2 ? 2 * (j % 2) + c : c);
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -425,15 +511,15 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             const int tok = (tb0 + wt * TB + t) * 16 + n;
-            if (tok < a.T) finish4<T>(a, tok, r, inv[tok], acc[b][t], par);
+            if (tok < a.T) finish4<T, offset_codes(BITS, T::bytes)>(a, tok, r, info[tok].inv, acc[b][t], par);
         }
     }
 }
 
 // The sum of the parts of K in their order, and the epilogue: four rows a thread.
 constexpr int kJoinThreads = 256;
-template <typename T>
-__global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const float* __restrict__ inv,
+template <typename T, int BITS>
+__global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const Row* __restrict__ info,
                                                             const float* __restrict__ part, int splits) {
     const int quads = (a.N + 3) / 4, blocks = (quads + kJoinThreads - 1) / kJoinThreads;
     const int t = blockIdx.x / blocks, r = (blockIdx.x % blocks * kJoinThreads + threadIdx.x) * 4;
@@ -443,7 +529,7 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const 
     floatx4 v = p[0];
 #pragma unroll 4
     for (int s = 1; s < splits; ++s) v += p[(int64_t)s * a.T * quads];
-    finish4<T>(a, t, r, inv[t], v, par);
+    finish4<T, offset_codes(BITS, T::bytes)>(a, t, r, info[t].inv, v, par);
 }
 
 // ------------------------------------------------------------- some tokens
@@ -458,7 +544,7 @@ constexpr int kRowFlight = 4;               // even: the operands' two buffers a
 template <typename T, int BITS, int TB, int NB>
 __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, const half8* __restrict__ hi,
                                                                  const half8* __restrict__ lo,
-                                                                 const float* __restrict__ inv, int calls) {
+                                                                 const Row* __restrict__ info, int calls) {
     using M = MfmaCodec<BITS>;
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
@@ -479,9 +565,11 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
     if (wave < kFinish) par = load_params(a, r0 + 16 * fb + 4 * g);
     floatx4 acc[TB][NB];
 #pragma unroll
-    for (int t = 0; t < TB; ++t)
+    for (int t = 0; t < TB; ++t) {
+        const float s = wave == 0 ? info[min(t, last_tb) * 16 + n].start : 0.f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) acc[t][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < NB; ++b) acc[t][b] = floatx4{s, s, s, s};
+    }
     // the planes' operands of a chunk, one chunk ahead
     constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
     half8 xv[2][M::NCALL][TB][kPlanes];
@@ -506,7 +594,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
             for (int c = 0; c < M::NCALL; ++c) {
                 half8 w[NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) w[b] = a_operand<BITS>(q[i][b], c);
+                for (int b = 0; b < NB; ++b) w[b] = a_operand<BITS, offset_codes(BITS, T::bytes)>(q[i][b], c);
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -532,7 +620,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
 #pragma unroll
     for (int w = 1; w < kRowWaves; ++w) v += part[w][wave][lane];
     const int tok = ft * 16 + n;
-    if (tok < a.T) finish4<T>(a, tok, r0 + 16 * fb + 4 * g, inv[tok], v, par);
+    if (tok < a.T) finish4<T, offset_codes(BITS, T::bytes)>(a, tok, r0 + 16 * fb + 4 * g, info[tok].inv, v, par);
 }
 
 // -------------------------------------------------------------- few tokens
@@ -553,6 +641,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
     constexpr int CW = 128 / BITS;
     constexpr int kThreads = kRowWaves * kWave;
     constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
+    constexpr bool kOffset = offset_codes(BITS, T::bytes);
     extern __shared__ half8 xs[];                          // [token][plane][call][lane group]
     __shared__ unsigned top[kFewTokens];                   // largest magnitudes as bits (they are not negative)
     __shared__ floatx4 part[kRowWaves][kWave];
@@ -602,7 +691,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
         if (k < total) {
             const int t = k / units;
             half8 h, l;
-            split_unit<BITS>(v[i], pow2(row_exponent(__uint_as_float(top[t]))), h, l);
+            split_unit<BITS, kOffset>(v[i], pow2(row_exponent(__uint_as_float(top[t]))), h, l);
             xs[kPlanes * t * units + k - t * units] = h;
             if (kPlanes == 2) xs[(2 * t + 1) * units + k - t * units] = l;
         }
@@ -611,6 +700,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
 
     const int tok = kPlanes == 2 ? n & 7 : n;
     const half8* mine = xs + (kPlanes * min(tok, a.T - 1) + (kPlanes == 2 ? n >> 3 : 0)) * units + g;
+    const half8 offset = minus_offset<BITS>();
     floatx4 acc2[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     for (int c0 = wave; c0 < chunks; c0 += kFewFlight * kRowWaves) {
 #pragma unroll
@@ -618,8 +708,15 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
             const int ch = c0 + i * kRowWaves;
             if (ch < chunks) {
 #pragma unroll
-                for (int c = 0; c < M::NCALL; ++c)
-                    acc2[c & 1] = mfma::mfma(a_operand<BITS>(q[i], c), mine[(ch * M::NCALL + c) * 4], acc2[c & 1]);
+                for (int c = 0; c < M::NCALL; ++c) {
+                    const half8 xv = mine[(ch * M::NCALL + c) * 4];
+                    if (kOffset) {
+                        acc2[0] = mfma::mfma(a_operand<BITS, kOffset>(q[i], c), xv, acc2[0]);
+                        acc2[1] = mfma::mfma(offset, xv, acc2[1]);     // the offset's part of the sum
+                    } else {
+                        acc2[c & 1] = mfma::mfma(a_operand<BITS, kOffset>(q[i], c), xv, acc2[c & 1]);
+                    }
+                }
             }
             const int nx = ch + kFewFlight * kRowWaves;
             if (nx < chunks) q[i] = ld16(wrow + (int64_t)min(4 * nx + g, groups - 1) * 16);
@@ -636,7 +733,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
         for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor(sum[i], 8, kWave);
     }
     if (tok >= a.T || (kPlanes == 2 && n >= 8)) return;
-    finish4<T>(a, tok, r0 + 4 * g, pow2(-row_exponent(__uint_as_float(top[tok]))), sum, par);
+    finish4<T, offset_codes(BITS, T::bytes)>(a, tok, r0 + 4 * g, pow2(-row_exponent(__uint_as_float(top[tok]))), sum, par);
 }
 
 // ------------------------------------------------------------------- launches
@@ -682,51 +779,51 @@ Tiling tiling(int64_t T, int64_t K, int64_t N, int bits, int bytes) {
 }
 
 template <typename T, int BITS, int NB, int TB, int WN, int WT, int D>
-void launch_gemm(const LinearArgs& a, const half8* hi, const half8* lo, const float* inv, float* part, int calls,
+void launch_gemm(const LinearArgs& a, const half8* hi, const half8* lo, const Row* info, float* part, int calls,
                  int splits, hipStream_t st) {
     const int64_t tiles = (int64_t)((a.N + WN * NB * 16 - 1) / (WN * NB * 16)) *
                           ((a.T + WT * TB * 16 - 1) / (WT * TB * 16)) * splits;
     hipLaunchKernelGGL((linear_gemm<T, BITS, NB, TB, WN, WT, D>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                       dim3(WN * WT * kWave), 0, st, a, hi, lo, inv, part, calls, splits);
+                       dim3(WN * WT * kWave), 0, st, a, hi, lo, info, part, calls, splits);
     if (splits > 1) {
         const int64_t blocks = ((a.N + 3) / 4 + kJoinThreads - 1) / kJoinThreads;
-        hipLaunchKernelGGL((linear_join<T>), dim3((unsigned)(blocks * a.T)), dim3(kJoinThreads), 0, st, a, inv, part,
+        hipLaunchKernelGGL((linear_join<T, BITS>), dim3((unsigned)(blocks * a.T)), dim3(kJoinThreads), 0, st, a, info, part,
                            splits);
     }
 }
 
 template <typename T, int BITS, int NU, int WPT>
-void launch_units(const LinearArgs& a, half8* hi, half8* lo, float* inv, int calls, hipStream_t st) {
+void launch_units(const LinearArgs& a, half8* hi, half8* lo, Row* info, int calls, hipStream_t st) {
     const int64_t grid = (blocks16(a.T) + 7) / 8 * 8 * (16 / (kPrepThreads / kWave / WPT));
     hipLaunchKernelGGL((linear_prepare<T, BITS, NU, WPT>), dim3((unsigned)grid), dim3(kPrepThreads), 0, st,
-                       reinterpret_cast<const typename T::type*>(a.x), a.ldx, a.T, a.K, calls, hi, lo, inv);
+                       reinterpret_cast<const typename T::type*>(a.x), a.ldx, a.T, a.K, calls, hi, lo, info);
 }
 
 // Four waves a token while that fills the compute units no more than a few times
 // over (4 us instead of 8 for 16 tokens of 6144 columns), else one.
 template <typename T, int BITS>
-void launch_prepare(const LinearArgs& a, half8* hi, half8* lo, float* inv, int calls, hipStream_t st) {
+void launch_prepare(const LinearArgs& a, half8* hi, half8* lo, Row* info, int calls, hipStream_t st) {
     const int units = calls * 4;
     if (a.T <= 1024) {
-        if (units <= 256) launch_units<T, BITS, 1, 4>(a, hi, lo, inv, calls, st);
-        else if (units <= 1024) launch_units<T, BITS, 4, 4>(a, hi, lo, inv, calls, st);
-        else launch_units<T, BITS, 0, 4>(a, hi, lo, inv, calls, st);
+        if (units <= 256) launch_units<T, BITS, 1, 4>(a, hi, lo, info, calls, st);
+        else if (units <= 1024) launch_units<T, BITS, 4, 4>(a, hi, lo, info, calls, st);
+        else launch_units<T, BITS, 0, 4>(a, hi, lo, info, calls, st);
     } else {
-        if (units <= 256) launch_units<T, BITS, 4, 1>(a, hi, lo, inv, calls, st);
-        else if (units <= 1024) launch_units<T, BITS, 16, 1>(a, hi, lo, inv, calls, st);
-        else launch_units<T, BITS, 0, 4>(a, hi, lo, inv, calls, st);
+        if (units <= 256) launch_units<T, BITS, 4, 1>(a, hi, lo, info, calls, st);
+        else if (units <= 1024) launch_units<T, BITS, 16, 1>(a, hi, lo, info, calls, st);
+        else launch_units<T, BITS, 0, 4>(a, hi, lo, info, calls, st);
     }
 }
 
 template <typename T, int BITS, int TB>
-void launch_rows(const LinearArgs& a, const half8* hi, const half8* lo, const float* inv, int calls, hipStream_t st) {
+void launch_rows(const LinearArgs& a, const half8* hi, const half8* lo, const Row* info, int calls, hipStream_t st) {
     // two row blocks a workgroup where that still gives every compute unit one
     if (a.N >= kCus * 32)
         hipLaunchKernelGGL((linear_rows<T, BITS, TB, 2>), dim3((a.N + 31) / 32), dim3(kRowWaves * kWave), 0, st, a, hi,
-                           lo, inv, calls);
+                           lo, info, calls);
     else
         hipLaunchKernelGGL((linear_rows<T, BITS, TB, 1>), dim3((a.N + 15) / 16), dim3(kRowWaves * kWave), 0, st, a, hi,
-                           lo, inv, calls);
+                           lo, info, calls);
 }
 
 template <typename T, int BITS>
@@ -741,17 +838,17 @@ hipError_t launch_bits(const LinearArgs& a, hipStream_t st) {
     const int64_t blocks = blocks16(a.T);
     half8* hi = reinterpret_cast<half8*>(a.workspace);
     half8* lo = hi + (T::bytes == 4 ? blocks * calls * kWave : 0);
-    float* inv = reinterpret_cast<float*>(lo + blocks * calls * kWave);
-    float* part = inv + blocks * 16;
-    launch_prepare<T, BITS>(a, hi, lo, inv, calls, st);
+    Row* info = reinterpret_cast<Row*>(lo + blocks * calls * kWave);
+    float* part = reinterpret_cast<float*>(info + blocks * 16);
+    launch_prepare<T, BITS>(a, hi, lo, info, calls, st);
     if (a.T <= 16) {
-        launch_rows<T, BITS, 1>(a, hi, lo, inv, calls, st);
+        launch_rows<T, BITS, 1>(a, hi, lo, info, calls, st);
     } else if (a.T <= kRowsTokens) {
-        launch_rows<T, BITS, 2>(a, hi, lo, inv, calls, st);
+        launch_rows<T, BITS, 2>(a, hi, lo, info, calls, st);
     } else {
         const Tiling k = tiling(a.T, a.K, a.N, BITS, T::bytes);
-        if (k.large) launch_gemm<T, BITS, 4, 8, 4, 2, 2>(a, hi, lo, inv, part, calls, k.splits, st);
-        else launch_gemm<T, BITS, 1, 4, 8, 1, 4>(a, hi, lo, inv, part, calls, k.splits, st);
+        if (k.large) launch_gemm<T, BITS, 4, 8, 4, 2, 2>(a, hi, lo, info, part, calls, k.splits, st);
+        else launch_gemm<T, BITS, 1, 4, 8, 1, 4>(a, hi, lo, info, part, calls, k.splits, st);
     }
     return hipGetLastError();
 }
@@ -771,7 +868,7 @@ hipError_t launch_type(int bits, const LinearArgs& a, hipStream_t st) {
 int64_t linear_workspace(int bits, int dtype, int64_t T, int64_t K, int64_t N) {
     const int bytes = dtype == MOEDEC_F32 ? 4 : 2;
     if (T == 0 || few(T, K, bits, bytes)) return 0;
-    int64_t n = blocks16(T) * 16 * (padded(K, bits) * bytes + 4);
+    int64_t n = blocks16(T) * 16 * (padded(K, bits) * bytes + (int64_t)sizeof(Row));
     if (T > kRowsTokens) {
         const int splits = tiling(T, K, N, bits, bytes).splits;
         if (splits > 1) n += splits * T * ((N + 3) / 4 * 16);

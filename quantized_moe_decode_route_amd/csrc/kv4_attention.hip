@@ -4,7 +4,13 @@
 //   p = exp2(S * scale * log2 e - M_m),  O[m] = sum_j (p * s_v[j]) * code_v[j] / sum_j p
 //
 // The row scales factor out of both products, so the matrix cores work on the
-// codes themselves, which are exact in fp16.  A row m is one query head of one
+// codes themselves, which are exact in fp16.  With 16-bit queries the keys' codes
+// enter as unsigned fields in fp16 subnormals, 5 instructions a word instead of 9
+// (u = code + 8 at bit 0 or 4 of its half is u * 2^-24 or u * 2^-20; the 2^4 is
+// taken out of the query element that meets it, the offset out of the start of the
+// sum, which is -8 times the sum of the row's queries and as such the product's
+// free addend); the terms grow fourfold, the rounding of the fp32 sums with them,
+// far below that of the 16-bit result.  A row m is one query head of one
 // token; 16 rows that share a key/value head are the N side of the products
 // (B operand), 32 keys at a time the M side of S^T = K Q^T and the K side of
 // O^T = V^T P^T.  In S^T a lane holds one row (lane % 16) and, with the tokens
@@ -131,6 +137,15 @@ __device__ __forceinline__ Tile find_tile(const Cache& c, const AttnArgs& a, int
     return t;
 }
 
+// The eight codes of a word as unsigned fields: element e is (code + 8) *
+// 2^(field_bit(e) - 24).
+__device__ __forceinline__ half8 codes_unsigned(uint32_t w) {
+    const uint32_t h = w >> 8;
+    return __builtin_bit_cast(half8, u32x4{(w & 0x000F000Fu) ^ 0x00080008u, (w & 0x00F000F0u) ^ 0x00800080u,
+                                           (h & 0x000F000Fu) ^ 0x00080008u, (h & 0x00F000F0u) ^ 0x00800080u});
+}
+__device__ __forceinline__ constexpr int field_bit(int e) { return e & 2 ? 4 : 0; }
+
 // Waves a SIMD is to hold (the register budget): as many as the accumulators allow
 // without spilling.
 constexpr int waves_per_simd(int D, int NT) { return D == 64 && NT <= 2 ? 4 : D <= 128 && NT == 1 ? 4 : 2; }
@@ -138,7 +153,7 @@ constexpr int waves_per_simd(int D, int NT) { return D == 64 && NT <= 2 ? 4 : D 
 // One split of one tile of one key/value head.
 template <typename T, int D, int NT>
 __global__ __launch_bounds__(kThreads, waves_per_simd(D, NT)) void kv4_attention_kernel(Cache c, AttnArgs a, int splits) {
-    constexpr bool kPair = T::bytes == 4;
+    constexpr bool kPair = T::bytes == 4, kOffset = !kPair;
     constexpr int kP = kPair ? 2 : 1;
     constexpr int kS = D / 32;            // MFMAs of a score, K side
     constexpr int kH = D / 64;            // 64-column parts of the output
@@ -146,7 +161,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, NT)) void kv4_attention
     constexpr int kLd = D + 4;
     __shared__ half8 qs[NT][kS][kP][kWave];
     __shared__ float so[kRT][kLd];
-    __shared__ float scm[kRT], sm[kWaves][kRT], sl[kWaves][kRT];
+    __shared__ float scm[kRT], sstart[kRT], sm[kWaves][kRT], sl[kWaves][kRT];
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, g = lane >> 4;
     const int head = blockIdx.x % c.kv_heads, sp = blockIdx.x / c.kv_heads % splits;
@@ -209,22 +224,30 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, NT)) void kv4_attention
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
         const int k = row_exponent(m);
         const float f = a.scale < 0.f ? -pow2(k) : pow2(k);
+        float sum = 0.f;
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
             half8 h, l;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float v = x[s][e] * f;
+                float v = x[s][e] * (kOffset && field_bit(e) ? f * 0.0625f : f);
                 if (kPair) asm volatile("" : "+v"(v));          // one rounding for both halves
                 const _Float16 hv = (_Float16)v;
                 h[e] = hv;
+                sum += (float)hv * (float)(1 << field_bit(e));
                 l[e] = (_Float16)(v - (float)hv);
             }
             qs[nt][s][0][lane] = h;
             if (kPair) qs[nt][s][kP - 1][lane] = l;
         }
         // never 0: the score of an unseen key is -inf times cm
-        if (g == 0) scm[16 * nt + n] = fmaxf(pow2(-k) * fabsf(a.scale) * kLog2e, 0x1p-126f);
+        // (kOffset: half of the sums' 2^24, the other half goes to the keys' scales)
+        if (g == 0) scm[16 * nt + n] = fmaxf(pow2(-k) * fabsf(a.scale) * kLog2e * (kOffset ? 0x1p12f : 1.f), 0x1p-126f);
+        if (kOffset) {
+            sum += __shfl_xor(sum, 16, kWave);
+            sum += __shfl_xor(sum, 32, kWave);
+            if (g == 0) sstart[16 * nt + n] = sum * (-8.f * 0x1p-24f);
+        }
     }
 
     __syncthreads();                       // queries staged
@@ -243,8 +266,13 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, NT)) void kv4_attention
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][h][j] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
-    floatx4 zero = {0.f, 0.f, 0.f, 0.f};           // held in registers: the first product's addend
-    asm volatile("" : "+v"(zero));
+    floatx4 start[NT];                     // the first product's addend, held in registers
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const float v = kOffset ? sstart[16 * i + n] : 0.f;
+        start[i] = floatx4{v, v, v, v};
+        asm volatile("" : "+v"(start[i]));
+    }
     float vref = 0x1p-100f, vinv = 0x1p105f;       // value scales enter as s_v * vinv <= 2^5, vinv = 2^5 / vref
 
     for (int step = 0; step < steps; ++step) {
@@ -276,22 +304,25 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, NT)) void kv4_attention
         floatx4 sc[NT][2];
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            const half8 kf0 = codes_f16(kw[0].w[s]), kf1 = codes_f16(kw[1].w[s]);
+            const half8 kf0 = kOffset ? codes_unsigned(kw[0].w[s]) : codes_f16(kw[0].w[s]);
+            const half8 kf1 = kOffset ? codes_unsigned(kw[1].w[s]) : codes_f16(kw[1].w[s]);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
                     const half8 q = qs[i][s][p][lane];
-                    sc[i][0] = mfma16(kf0, q, s == 0 && p == 0 ? zero : sc[i][0]);
-                    sc[i][1] = mfma16(kf1, q, s == 0 && p == 0 ? zero : sc[i][1]);
+                    sc[i][0] = mfma16(kf0, q, s == 0 && p == 0 ? start[i] : sc[i][0]);
+                    sc[i][1] = mfma16(kf1, q, s == 0 && p == 0 ? start[i] : sc[i][1]);
                 }
         }
         bool move = false;
-        float z[NT][8], mx[NT];
+        float z[NT][8], mx[NT], kscale[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) kscale[e] = __uint_as_float(ks.w[e]) * (kOffset ? 0x1p12f : 1.f);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[i][e] = sc[i][e >> 2][e & 3] * __uint_as_float(ks.w[e]);
+            for (int e = 0; e < 8; ++e) z[i][e] = sc[i][e >> 2][e & 3] * kscale[e];
             if (edge) {
                 asm volatile("");                  // a branch, not selects in every step
 #pragma unroll
