@@ -148,11 +148,13 @@ __device__ __forceinline__ constexpr int field_bit(int e) { return e & 2 ? 4 : 0
 
 // Waves a SIMD is to hold (the register budget): as many as the accumulators allow
 // without spilling.
-constexpr int waves_per_simd(int D, int NT) { return D == 64 && NT <= 2 ? 4 : D <= 128 && NT == 1 ? 4 : 2; }
+constexpr int waves_per_simd(int D, int NT, bool pair) {
+    return D <= 128 && NT == 1 ? 4 : D == 64 ? (pair ? 4 : 3) : 2;
+}
 
 // One split of one tile of one key/value head.
 template <typename T, int D, int NT>
-__global__ __launch_bounds__(kThreads, waves_per_simd(D, NT)) void kv4_attention_kernel(Cache c, AttnArgs a, int splits) {
+__global__ __launch_bounds__(kThreads, waves_per_simd(D, NT, T::bytes == 4)) void kv4_attention_kernel(Cache c, AttnArgs a, int splits) {
     constexpr bool kPair = T::bytes == 4, kOffset = !kPair;
     constexpr int kP = kPair ? 2 : 1;
     constexpr int kS = D / 32;            // MFMAs of a score, K side
@@ -582,9 +584,9 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_join(Cache c, AttnArgs
 
 // How a call is cut: 16-row blocks of a workgroup by the rows a sequence has on
 // average (prompts: three at head_dim 128, where four spilled registers, 614
-// against 587 us for 2 x 1500 queries of 48 heads over 6000 keys, and two
-// elsewhere: at 64 two with four waves a SIMD took 55 us for 3 x 1000 queries of 8
-// heads over 3000 keys, four with two waves 68), and splits of the keys: enough workgroups for four
+// against 587 us for 2 x 1500 queries of 48 heads over 6000 keys, now 530, and two
+// elsewhere: at 64 two took 64 us for 3 x 1000 queries of 8 heads over 3000 keys,
+// three 70), and splits of the keys: enough workgroups for four
 // on every compute unit if the splits keep kMinChunk keys, and four times as many,
 // which evens out ragged lengths, if they keep eight times that.  Up to kNoSplit keys
 // the second launch would cost more than it saves.

@@ -565,6 +565,12 @@ class KvCache:
 
 
 
+def _layer(cache: "KvCache", layer: int) -> int:
+    if not 0 <= layer < cache.data.shape[0]:
+        raise ValueError(f"layer must be in [0, {cache.data.shape[0]})")
+    return layer
+
+
 def _ints(t: torch.Tensor | None, name: str, dev: torch.device, n: int) -> int | None:
     return None if t is None else _on(t, torch.int32, name, dev, (n,))
 
@@ -579,7 +585,7 @@ def kv4_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor, q_s
     vp, ldv = _rows(v, inner, "v", dev)
     if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
         raise ValueError("k and v must have one dtype and as many rows")
-    _launch("kv4_append", dev, ctypes.byref(c), layer, kp, ldk, vp, ldv, DTYPES[k.dtype], k.shape[0],
+    _launch("kv4_append", dev, ctypes.byref(c), _layer(cache, layer), kp, ldk, vp, ldv, DTYPES[k.dtype], k.shape[0],
             _ints(q_start, "q_start", dev, c.n_seqs + 1), _ints(granted, "granted", dev, c.n_seqs))
 
 
@@ -594,7 +600,7 @@ def kv4_read(cache: KvCache, layer: int, first: torch.Tensor, q_start: torch.Ten
         raise ValueError("rows must not be negative")
     k, v = (torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev) for _ in range(2))
     ld = cache.kv_heads * cache.head_dim
-    _launch("kv4_read", dev, ctypes.byref(c), layer, _ints(first, "first", dev, c.n_seqs),
+    _launch("kv4_read", dev, ctypes.byref(c), _layer(cache, layer), _ints(first, "first", dev, c.n_seqs),
             _ints(q_start, "q_start", dev, c.n_seqs + 1), rows, k.data_ptr(), ld, v.data_ptr(), ld,
             DTYPES[dtype])
     return k, v
@@ -613,6 +619,8 @@ def kv4_attention(q: torch.Tensor, cache: KvCache, layer: int, q_start: torch.Te
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
     rows, heads = q.shape[0], q.shape[1]
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window must be in [0, 2^31)")
     qp, ldq = _rows(q, (heads, cache.head_dim), "q", dev)
     if out is None:
         out = torch.empty((rows, heads, cache.head_dim), dtype=q.dtype, device=dev)
@@ -624,7 +632,7 @@ def kv4_attention(q: torch.Tensor, cache: KvCache, layer: int, q_start: torch.Te
     bound = cap if max_len is None else min(int(max_len), cap)
     nb = lib().kv4_attention_workspace(ctypes.byref(c), rows, heads, bound)
     ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb > 0 else None
-    _launch("kv4_attention", dev, ctypes.byref(c), layer, qp, ldq, DTYPES[q.dtype], rows, heads,
+    _launch("kv4_attention", dev, ctypes.byref(c), _layer(cache, layer), qp, ldq, DTYPES[q.dtype], rows, heads,
             _ints(q_start, "q_start", dev, c.n_seqs + 1), _ints(granted, "granted", dev, c.n_seqs),
             cache.head_dim ** -0.5 if scale is None else float(scale), window, bound, op, ldo, lp,
             ws.data_ptr() if nb > 0 else None, max(nb, 0))

@@ -233,3 +233,65 @@ def test_two_streams_at_once():
             got.append(ops.kv4_attention(q, cache, 0, start))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in got)
+
+
+def test_pool_past_32_bits():
+    """Pages that lie beyond 4 GB of the pool, in its second layer."""
+    dim, heads, page = 128, 8, 128
+    unit = page * heads * (dim + 8)
+    n_pages = (3 << 30) // unit + 1
+    cache = ops.KvCache.allocate(2, n_pages, page, heads, dim, 2, 8, DEV)
+    lens = [300, 129]
+    cache.table[0, :3] = ints([n_pages - 1, 0, n_pages - 3])
+    cache.table[1, :2] = ints([n_pages - 2, n_pages // 2])
+    cache.len.copy_(ints(lens))
+    rng = np.random.default_rng(17)
+    held = fill(cache, lens, rng, layer=1)
+    k, v = ops.kv4_read(cache, 1, ints([0, 0]), ints(starts(lens)), sum(lens))
+    assert np.array_equal(k.cpu().numpy(), np.concatenate([h[0] for h in held]))
+    assert np.array_equal(v.cpu().numpy(), np.concatenate([h[1] for h in held]))
+    q = rows(rng, 2, 16, dim, "f32", strong=False)
+    out = ops.kv4_attention(q.to(DEV), cache, 1, ints([0, 1, 2])).double().cpu().numpy()
+    for s, n in enumerate(lens):
+        kk, vv = (x.astype(np.float64) for x in held[s])
+        o, _, mag, dots = aorc.attention(q[s:s + 1].double().numpy(), kk, vv, n - 1, dim ** -0.5)
+        assert (np.abs(out[s:s + 1] - o) <= attention_bound(mag, dots, o, n, dim, "f32")).all()
+
+
+def test_long_flat_cache():
+    """200,000 keys of nearly equal weight in one sequence: the sums and the joins
+    of many splits keep their digits."""
+    n = 200_000
+    cache = new_cache([n], 128, 1, 64)
+    rng = np.random.default_rng(18)
+    (k, v), = fill(cache, [n], rng)
+    for dtype in ("f32", "bf16"):
+        q = rows(rng, 1, 2, 64, dtype, strong=False)
+        out = ops.kv4_attention(q.to(DEV), cache, 0, ints([0, 1]), scale=0.01).double().cpu().numpy()
+        o, _, mag, dots = aorc.attention(q.double().numpy(), k.astype(np.float64), v.astype(np.float64), n - 1, 0.01)
+        # the probabilities' roundings are independent: their part of the bound falls with
+        # the root of the keys (six standard deviations), the sums' stays
+        p = 2.0 ** -21 if dtype == "f32" else 2.0 ** -11
+        loose = attention_bound(mag, dots, o, 64, 64, dtype) - mag * p
+        assert (np.abs(out - o) <= loose + mag * (6 * p / np.sqrt(n) + 2.0 ** -17)).all()
+
+
+def test_binding_refuses():
+    cache = new_cache([4], 32)
+    q, start = torch.zeros((1, 4, 64), device=DEV), ints([0, 1])
+    for bad in (dict(window=-1), dict(window=1 << 31), dict(window=(1 << 32) + 5), dict(max_len=0)):
+        with pytest.raises((ValueError, ops.MoedecError)):
+            ops.kv4_attention(q, cache, 0, start, **bad)
+    for layer in (-1, 1, 1 << 32):
+        with pytest.raises(ValueError):
+            ops.kv4_attention(q, cache, layer, start)
+    with pytest.raises(ValueError):
+        ops.kv4_attention(q, cache, 0, start.long())
+    with pytest.raises(ValueError):
+        ops.kv4_attention(q[:, :, :32], cache, 0, start)
+    with pytest.raises(ValueError):
+        ops.kv4_attention(q.transpose(1, 2).contiguous().transpose(1, 2), cache, 0, start)
+    with pytest.raises(ops.MoedecError):
+        ops.kv4_attention(torch.zeros((1, 3, 64), device=DEV), cache, 0, start)    # 3 heads over 2
+    with pytest.raises(ops.MoedecError):
+        ops.kv4_attention(torch.zeros((2, 5 * 64 + 1), device=DEV)[:, 1:257].unflatten(1, (4, 64)), cache, 0, start)

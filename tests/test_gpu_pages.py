@@ -146,6 +146,17 @@ def test_large_pool_lowest_first():
     b.reserve([32, 0, 0, 1])
 
 
+def test_most_sequences():
+    """1024 sequences, many sharing one page, and a pool that ends inside the call."""
+    b = Both(1500, 1024, 4, layers=1)
+    b.reserve([40] + [0] * 1023)
+    b.fork([0] * 600, list(range(1, 601)))
+    b.reserve([1] * 1024)
+    b.reserve([20 if s % 3 else 0 for s in range(1024)])
+    b.truncate([0 if s % 2 else -1 for s in range(1024)])
+    b.compact()
+
+
 @pytest.mark.parametrize("seed", range(4))
 def test_random_walk(seed):
     rng = np.random.default_rng(seed)
