@@ -534,7 +534,7 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const 
 
 // ------------------------------------------------------------- some tokens
 //
-// Up to TB * 16 tokens: bound by the weights' bytes and the planes' L2 reads.  A
+// Up to TB * 16 tokens (64, 32 in fp32): bound by the weights' bytes and the planes' L2 reads.  A
 // workgroup owns NB * 16 weight rows and all tokens; its waves split K by chunks
 // of 64 bytes of a row, all loads linear, kRowFlight chunks of codes in flight,
 // and meet in LDS in a fixed order.
@@ -625,15 +625,15 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
 
 // -------------------------------------------------------------- few tokens
 //
-// Up to kFewTokens tokens whose fp16 form fits in LDS, in one launch: every
+// Up to kFewTokens tokens of kFewValues values together, in one launch: every
 // workgroup converts the activations itself while its first weight loads are in
 // flight.  With one to eight tokens the 16 MFMA columns hold the hi parts (0 ..
 // 7) and, for fp32, the lo parts (8 .. 15) side by side, so a pair costs no
 // second MFMA; columns without a token repeat one and are dropped.
 constexpr int kFewTokens = 8;
-constexpr int kFewLds = 64 * 1024;
+constexpr int kFewValues = 16384;         // tokens times padded columns at most
 constexpr int kFewFlight = 8;             // chunks a wave has in flight
-constexpr int kFewUnits = 8;              // units a thread converts at most
+constexpr int kFewUnits = kFewValues / 8 / (kRowWaves * kWave);   // units a thread converts at most
 
 template <typename T, int BITS>
 __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, int calls) {
@@ -738,13 +738,15 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
 
 // ------------------------------------------------------------------- launches
 
-constexpr int kRowsTokens = 32;           // linear_rows up to here
+// linear_rows up to here: as many blocks of 16 tokens as keep a chunk's operands in
+// registers, twice (64 bf16 tokens of 6144 -> 8192 in int4: 20 us, 25 by linear_gemm).
+constexpr int rows_tokens(int bytes) { return bytes == 4 ? 32 : 64; }
 constexpr int kCus = 256;
 
-bool few(int64_t T, int64_t K, int bits, int bytes) {
-    const int64_t n = T * padded(K, bits);
-    return T <= kFewTokens && n * (bytes == 4 ? 4 : 2) <= kFewLds && n / 8 <= kFewUnits * kRowWaves * kWave;
-}
+// The one-launch form: every workgroup converts all activations, so it pays while
+// they are few (int4, bf16, 4096 -> 4096, 4 tokens: 7.6 us against 8.6 by way of
+// planes; 6144 -> 8192, 4 tokens: 14.2 against 12.6).
+bool few(int64_t T, int64_t K, int bits) { return T <= kFewTokens && T * padded(K, bits) <= kFewValues; }
 
 // The tile of linear_gemm and the parts of K.  Two tiles: 128 weight rows by 64
 // tokens, of which a compute unit holds two (sixteen waves hide the loads of short
@@ -830,7 +832,7 @@ template <typename T, int BITS>
 hipError_t launch_bits(const LinearArgs& a, hipStream_t st) {
     const int64_t Kp = padded(a.K, BITS);
     const int calls = (int)(Kp / 32);
-    if (few(a.T, a.K, BITS, T::bytes)) {
+    if (few(a.T, a.K, BITS)) {
         const size_t lds = (size_t)a.T * Kp * (T::bytes == 4 ? 4 : 2);
         hipLaunchKernelGGL((linear_few<T, BITS>), dim3((a.N + 15) / 16), dim3(kRowWaves * kWave), lds, st, a, calls);
         return hipGetLastError();
@@ -843,8 +845,13 @@ hipError_t launch_bits(const LinearArgs& a, hipStream_t st) {
     launch_prepare<T, BITS>(a, hi, lo, info, calls, st);
     if (a.T <= 16) {
         launch_rows<T, BITS, 1>(a, hi, lo, info, calls, st);
-    } else if (a.T <= kRowsTokens) {
+    } else if (a.T <= 32) {
         launch_rows<T, BITS, 2>(a, hi, lo, info, calls, st);
+    } else if (a.T <= rows_tokens(T::bytes)) {
+        if constexpr (rows_tokens(T::bytes) > 32) {
+            if (a.T <= 48) launch_rows<T, BITS, 3>(a, hi, lo, info, calls, st);
+            else launch_rows<T, BITS, 4>(a, hi, lo, info, calls, st);
+        }
     } else {
         const Tiling k = tiling(a.T, a.K, a.N, BITS, T::bytes);
         if (k.large) launch_gemm<T, BITS, 4, 8, 4, 2, 2>(a, hi, lo, info, part, calls, k.splits, st);
@@ -867,9 +874,9 @@ hipError_t launch_type(int bits, const LinearArgs& a, hipStream_t st) {
 
 int64_t linear_workspace(int bits, int dtype, int64_t T, int64_t K, int64_t N) {
     const int bytes = dtype == MOEDEC_F32 ? 4 : 2;
-    if (T == 0 || few(T, K, bits, bytes)) return 0;
+    if (T == 0 || few(T, K, bits)) return 0;
     int64_t n = blocks16(T) * 16 * (padded(K, bits) * bytes + (int64_t)sizeof(Row));
-    if (T > kRowsTokens) {
+    if (T > rows_tokens(bytes)) {
         const int splits = tiling(T, K, N, bits, bytes).splits;
         if (splits > 1) n += splits * T * ((N + 3) / 4 * 16);
     }
