@@ -570,28 +570,37 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[t][b] = floatx4{s, s, s, s};
     }
-    // the planes' operands of a chunk, one chunk ahead
+    // the planes' operands of a chunk, one chunk ahead where they fit the registers
     constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
-    half8 xv[2][M::NCALL][TB][kPlanes];
-    auto acts = [&](half8 (*to)[TB][kPlanes], int ch) {
+    constexpr bool kAhead = M::NCALL * TB * kPlanes <= 16;
+    half8 xv[kAhead ? 2 : 1][kAhead ? M::NCALL : 1][TB][kPlanes];
+    auto call = [&](half8 (*to)[kPlanes], int ch, int c) {
 #pragma unroll
-        for (int c = 0; c < M::NCALL; ++c)
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                const int64_t at = ((int64_t)min(t, last_tb) * calls + ch * M::NCALL + c) * kWave + lane;
-                to[c][t][0] = hi[at];
-                if (kPlanes == 2) to[c][t][kPlanes - 1] = lo[at];
-            }
+        for (int t = 0; t < TB; ++t) {
+            const int64_t at = ((int64_t)min(t, last_tb) * calls + ch * M::NCALL + c) * kWave + lane;
+            to[t][0] = hi[at];
+            if (kPlanes == 2) to[t][kPlanes - 1] = lo[at];
+        }
     };
-    if (wave < chunks) acts(xv[0], wave);
+    auto acts = [&](int to, int ch) {
+#pragma unroll
+        for (int c = 0; c < M::NCALL; ++c) call(xv[to][c], ch, c);
+    };
+    if constexpr (kAhead) {
+        if (wave < chunks) acts(0, wave);
+    }
     for (int c0 = wave; c0 < chunks; c0 += kRowFlight * kRowWaves) {
 #pragma unroll
         for (int i = 0; i < kRowFlight; ++i) {
             const int ch = c0 + i * kRowWaves;
             if (ch >= chunks) break;
-            if (ch + kRowWaves < chunks) acts(xv[(i + 1) & 1], ch + kRowWaves);
+            if constexpr (kAhead) {
+                if (ch + kRowWaves < chunks) acts((i + 1) & 1, ch + kRowWaves);
+            }
 #pragma unroll
             for (int c = 0; c < M::NCALL; ++c) {
+                half8(*x)[kPlanes] = xv[kAhead ? i & 1 : 0][kAhead ? c : 0];
+                if constexpr (!kAhead) call(x, ch, c);
                 half8 w[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b) w[b] = a_operand<BITS, offset_codes(BITS, T::bytes)>(q[i][b], c);
@@ -600,7 +609,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
 #pragma unroll
                     for (int k = 0; k < kPlanes; ++k)
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) acc[t][b] = mfma::mfma(w[b], xv[i & 1][c][t][k], acc[t][b]);
+                        for (int b = 0; b < NB; ++b) acc[t][b] = mfma::mfma(w[b], x[t][k], acc[t][b]);
             }
             const int nx = ch + kRowFlight * kRowWaves;
             if (nx < chunks) {

@@ -9,7 +9,6 @@ fallback: if libmoedec.so is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 import re
 from dataclasses import dataclass
@@ -432,33 +431,32 @@ def _rows(t: torch.Tensor, inner: tuple, name: str, dev: torch.device) -> tuple[
     """Pointer and row stride of rows [n, *inner], each row contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device != dev or not t.is_cuda:
+    if t.device != dev or dev.type != "cuda":
         raise ValueError(f"{name} must be on {dev} (a GPU)")
     if t.dtype not in DTYPES:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 1 + len(inner) or shape[1:] != inner:
+    shape, ld = t.shape, t.stride()
+    if shape[1:] != inner or len(shape) == 0:
         raise ValueError(f"{name} must be [rows, {', '.join(map(str, inner))}], got {tuple(shape)}")
-    row = math.prod(inner)
-    if t.is_contiguous():
-        return t.data_ptr(), row
-    ld, step = t.stride(), 1
-    for i in range(len(inner), 0, -1):
-        if inner[i - 1] != 1 and ld[i] != step:
+    row = 1
+    for i in range(len(inner) - 1, -1, -1):
+        if ld[i + 1] != row and inner[i] != 1:
             raise ValueError(f"the rows of {name} must be contiguous")
-        step *= inner[i - 1]
+        row *= inner[i]
     return t.data_ptr(), (ld[0] if shape[0] > 1 else row)
 
 
 def _on(t: torch.Tensor, dtype: torch.dtype, name: str, dev: torch.device, shape: tuple) -> int:
     """Pointer of a contiguous tensor of that type, device and shape."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
-            and t.is_contiguous()):
-        _dev(t, dtype, name)
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}")
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 @dataclass
