@@ -1,17 +1,21 @@
 // y = act(scale * (x . codes) + bias) + residual on packed row-scaled weights.
 //
-// Codes.  A code q of b bits may enter as the unsigned u = q + 2^(b-1), isolated
-// with its sign bit flipped by one bit operation and left where it stands in the
-// low byte of its 16-bit half: read as fp16 that is the subnormal u * 2^j * 2^-24,
-// j its bit position, exactly.  The 2^j is taken out of the activation that meets
-// it, 2^24 out of the sum, and the offset out of the start of the sum,
+// Codes.  Beside 16-bit activations a code q of b bits enters as the unsigned u =
+// q + 2^(b-1), isolated with its sign bit flipped by one bit operation and left
+// where it stands in the low byte of its 16-bit half (2 bits: 3 bits higher): read
+// as fp16 that is u * 2^j * 2^-24, j its bit position, exactly, subnormal or just
+// above.  The 2^j is taken out of the activation that meets it, 2^24 out of the
+// sum, and the offset out of the start of the sum,
 //   sum x q = -2^(b-1) sum x + sum x u,
 // with sum x over the activations as they enter.  Converting 8 codes of 4 bits then
 // costs 5 vector instructions instead of 9, of 8 bits 6 instead of 10, of 2 bits
-// 4.5 instead of 12; but the terms are about four times as large for 4 and 8 bits
-// (1.5 times for 2), and the fp32 rounding of the sum with them.  That disappears
-// in a 16-bit result; fp32 results keep signed codes at 4 and 8 bits.  (int4, bf16,
-// 6144 -> 8192: 1024 tokens 136 us, 146 with signed codes, 4096 tokens 426 / 449.)
+// 5 instead of 12.  (int4, bf16, 6144 -> 8192: 1024 tokens 136 us, 146 with signed
+// codes, 4096 tokens 426 / 449.)  It costs bits of the sum: the matrix core aligns
+// products by their operands' exponent fields, so a subnormal's leading zeros are
+// lost below the largest product.  Measured against 64 bits, relative to the
+// result's rms: 1e-5 for 4 bits at K = 6144, where an fp16 result rounds by 2e-4 and
+// a bf16 one by 1.7e-3 (2 bits left in place: 3.3e-5, hence the 3 bits), but an
+// fp32 result by 2.5e-8.  fp32 keeps signed codes, whose sums are within 2e-7.
 //
 // Activations.  Every fp16 or bf16 activation is exact in fp16, up to the exponent
 // range, once its row is scaled by a power of two that brings the largest
@@ -34,15 +38,18 @@ namespace {
 
 using mfma::MfmaCodec;
 
-// Codes of a 32-bit word as unsigned fields in fp16 subnormals (see above): the
+// Codes of a 32-bit word as unsigned fields of fp16 patterns (see above): the
 // fields `mask` selects of both halves, their sign bits `flip` inverted.
 __device__ __forceinline__ uint32_t fields(uint32_t w, uint32_t mask, uint32_t flip) { return (w & mask) ^ flip; }
 
 // Whether codes enter as unsigned fields, for elements of that many bytes.
-constexpr bool offset_codes(int bits, int bytes) { return bits == 2 || bytes == 2; }
+constexpr bool offset_codes(int bytes) { return bytes == 2; }
+// The lowest bit position of a field in its half.
+constexpr int field_base(int bits) { return bits == 2 ? 3 : 0; }
 
 // Operand of call c of a 16-byte group of codes, in the element order of
-// MfmaCodec: element e holds u * 2^field_bit(e) * 2^-24 (kOffset) or q.
+// MfmaCodec: element e holds u * 2^(field_base + field_bit(e)) * 2^-24 (kOffset)
+// or q.
 template <int BITS, bool kOffset>
 __device__ __forceinline__ half8 a_operand(const uint4& q, int c) {
     if constexpr (!kOffset) {
@@ -59,13 +66,13 @@ __device__ __forceinline__ half8 a_operand(const uint4& q, int c) {
         p = u32x4{fields(w0, 0x00FF00FFu, 0x00800080u), fields(w0 >> 8, 0x00FF00FFu, 0x00800080u),
                   fields(w1, 0x00FF00FFu, 0x00800080u), fields(w1 >> 8, 0x00FF00FFu, 0x00800080u)};
     } else {
-        const uint32_t w = mfma::dword(q, c >> 1) >> (8 * (c & 1));
-        p = u32x4{fields(w, 0x00030003u, 0x00020002u), fields(w, 0x000C000Cu, 0x00080008u),
-                  fields(w, 0x00300030u, 0x00200020u), fields(w, 0x00C000C0u, 0x00800080u)};
+        const uint32_t d = mfma::dword(q, c >> 1), w = c & 1 ? d >> 5 : d << 3;
+        p = u32x4{fields(w, 0x00180018u, 0x00100010u), fields(w, 0x00600060u, 0x00400040u),
+                  fields(w, 0x01800180u, 0x01000100u), fields(w, 0x06000600u, 0x04000400u)};
     }
     return __builtin_bit_cast(half8, p);
 }
-// Bit position of element e's field in its half.
+// Bit position of element e's field above the lowest.
 template <int BITS, bool kOffset>
 __device__ __forceinline__ constexpr int field_bit(int e) {
     return !kOffset ? 0 : BITS == 4 ? 4 * ((e >> 1) & 1) : BITS == 2 ? 2 * (e >> 1) : 0;
@@ -78,7 +85,7 @@ __device__ __forceinline__ half8 minus_offset() {
     if constexpr (BITS == 4) p = u32x4{0x00080008u | sign, 0x00800080u | sign, 0x00080008u | sign, 0x00800080u | sign};
     else if constexpr (BITS == 8)
         p = u32x4{0x00800080u | sign, 0x00800080u | sign, 0x00800080u | sign, 0x00800080u | sign};
-    else p = u32x4{0x00020002u | sign, 0x00080008u | sign, 0x00200020u | sign, 0x00800080u | sign};
+    else p = u32x4{0x00100010u | sign, 0x00400040u | sign, 0x01000100u | sign, 0x04000400u | sign};
     return __builtin_bit_cast(half8, p);
 }
 
@@ -135,10 +142,12 @@ struct Four {
 };
 
 // The epilogue of rows r .. r+3 of token t.
-template <typename T, bool kOffset>
+template <typename T, int BITS>
 __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int r, float inv, const floatx4& sum,
                                         const Params& p) {
     if (r >= a.N) return;
+    constexpr bool kOffset = offset_codes(T::bytes);
+    constexpr float unit = (float)(1 << (24 - field_base(BITS)));
     typedef typename Four<T>::type four;
     typename T::type* y = reinterpret_cast<typename T::type*>(a.y) + (int64_t)t * a.ldy + r;
     const typename T::type* res = reinterpret_cast<const typename T::type*>(a.residual) + (int64_t)t * a.ldr + r;
@@ -147,7 +156,7 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int r, float
     if (a.residual && whole) old = *reinterpret_cast<const four*>(res);
     float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = sum[i] * (kOffset ? 0x1p24f : 1.f) * inv * p.scale[i] + p.bias[i];
+    for (int i = 0; i < 4; ++i) v[i] = sum[i] * (kOffset ? unit : 1.f) * inv * p.scale[i] + p.bias[i];
     if (a.act != MOEDEC_ACT_NONE) {                // uniform
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = activate(v[i], a.act);
@@ -251,7 +260,7 @@ __device__ __forceinline__ float max8(const float* v, float m) {
 // XCD), a few microseconds of latency for few: those take four waves a token.
 struct Row {
     float inv;                           // 1 / the row's power of two
-    float start;                         // of the sum: -2^(BITS-1) * 2^-24 times the sum of the row, or 0
+    float start;                         // of the sum: -2^(BITS-1) * 2^(field_base-24) times the sum of the row, or 0
 };
 
 template <typename T, int BITS, int NU, int WPT>
@@ -261,7 +270,7 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T:
     constexpr int kPer = kPrepThreads / kWave / WPT;       // tokens of a workgroup
     constexpr int kParts = 16 / kPer;                      // workgroups of a block of 16 tokens: all on one XCD
     constexpr int kLanes = WPT * kWave;
-    constexpr bool kOffset = offset_codes(BITS, T::bytes);
+    constexpr bool kOffset = offset_codes(T::bytes);
     __shared__ float red[kPrepThreads / kWave];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), j = threadIdx.x % kLanes;
     const int xcd = blockIdx.x % 8, i8 = blockIdx.x / 8;
@@ -323,7 +332,7 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prepare(const typename T:
     if (j == 0) {
         Row r;
         r.inv = pow2(-row_exponent(m));
-        r.start = kOffset ? sum * (-(float)(1 << (BITS - 1)) * 0x1p-24f) : 0.f;
+        r.start = kOffset ? sum * (-(float)(1 << (BITS - 1)) / (1 << (24 - field_base(BITS)))) : 0.f;
         info[t] = r;
     }
 }
@@ -374,7 +383,10 @@ __device__ __forceinline__ half8 step_operand(const Packed<BITS>& p, int c) {
 // tile is finished here, else its fp32 sums go to `part` [split][token][row].
 //
 // Bound by the matrix cores where tokens are many: a wave's step is 4 * NB * TB
-// MFMAs of 16 cycles against 4 * NB conversions of 9 vector instructions.
+// MFMAs of 16 cycles against 4 * NB conversions of 5 or 6 vector instructions.
+// 4096 tokens of 6144 -> 8192 in int4, bf16: 409 us, 1008 TF/s, of 1129 that a large
+// bf16 library product of 8192^3 reaches; 777 fp32 tokens of 2048 -> 6145 in int2: 70
+// us, 560 TF/s of the pair's products.
 // Workgroups are dealt to the eight XCDs in contiguous runs of tiles, four token
 // tiles by the weight tiles, so that an XCD's L2 serves each activation tile to
 // several workgroups.
@@ -482,7 +494,7 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
                 half8 w[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    w[b] = step_operand<BITS, offset_codes(BITS, T::bytes)>(pk[kMove ? 0 : kPlanes == 2 ? j / 2 : j % kPackRing][b], kPlanes == 2 ? 2 * (j % 2) + c : c);
+                    w[b] = step_operand<BITS, offset_codes(T::bytes)>(pk[kMove ? 0 : kPlanes == 2 ? j / 2 : j % kPackRing][b], kPlanes == 2 ? 2 * (j % 2) + c : c);
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -511,7 +523,7 @@ __global__ __launch_bounds__(WN * WT * kWave) void linear_gemm(LinearArgs a, con
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             const int tok = (tb0 + wt * TB + t) * 16 + n;
-            if (tok < a.T) finish4<T, offset_codes(BITS, T::bytes)>(a, tok, r, info[tok].inv, acc[b][t], par);
+            if (tok < a.T) finish4<T, BITS>(a, tok, r, info[tok].inv, acc[b][t], par);
         }
     }
 }
@@ -529,15 +541,17 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const 
     floatx4 v = p[0];
 #pragma unroll 4
     for (int s = 1; s < splits; ++s) v += p[(int64_t)s * a.T * quads];
-    finish4<T, offset_codes(BITS, T::bytes)>(a, t, r, info[t].inv, v, par);
+    finish4<T, BITS>(a, t, r, info[t].inv, v, par);
 }
 
 // ------------------------------------------------------------- some tokens
 //
-// Up to TB * 16 tokens (64, 32 in fp32): bound by the weights' bytes and the planes' L2 reads.  A
+// Up to TB * 16 tokens (64, 32 in fp32): bound by the weights' bytes and the planes'
+// L2 reads.  A
 // workgroup owns NB * 16 weight rows and all tokens; its waves split K by chunks
 // of 64 bytes of a row, all loads linear, kRowFlight chunks of codes in flight,
-// and meet in LDS in a fixed order.
+// and meet in LDS in a fixed order.  37 bf16 tokens of 2048 -> 6144 in int8: 8.5 us
+// after 2.5 us of planes.
 constexpr int kRowWaves = 8;
 constexpr int kRowFlight = 4;               // even: the operands' two buffers alternate with it
 
@@ -603,7 +617,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
                 if constexpr (!kAhead) call(x, ch, c);
                 half8 w[NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) w[b] = a_operand<BITS, offset_codes(BITS, T::bytes)>(q[i][b], c);
+                for (int b = 0; b < NB; ++b) w[b] = a_operand<BITS, offset_codes(T::bytes)>(q[i][b], c);
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -629,7 +643,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
 #pragma unroll
     for (int w = 1; w < kRowWaves; ++w) v += part[w][wave][lane];
     const int tok = ft * 16 + n;
-    if (tok < a.T) finish4<T, offset_codes(BITS, T::bytes)>(a, tok, r0 + 16 * fb + 4 * g, info[tok].inv, v, par);
+    if (tok < a.T) finish4<T, BITS>(a, tok, r0 + 16 * fb + 4 * g, info[tok].inv, v, par);
 }
 
 // -------------------------------------------------------------- few tokens
@@ -638,7 +652,9 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_rows(LinearArgs a, c
 // workgroup converts the activations itself while its first weight loads are in
 // flight.  With one to eight tokens the 16 MFMA columns hold the hi parts (0 ..
 // 7) and, for fp32, the lo parts (8 .. 15) side by side, so a pair costs no
-// second MFMA; columns without a token repeat one and are dropped.
+// second MFMA; columns without a token repeat one and are dropped.  One fp32 token
+// of 6144 -> 8192 in int4: 10.6 us, 2.4 TB/s of weights, of which the launch and the
+// first memory latencies are about half.
 constexpr int kFewTokens = 8;
 constexpr int kFewValues = 16384;         // tokens times padded columns at most
 constexpr int kFewFlight = 8;             // chunks a wave has in flight
@@ -650,7 +666,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
     constexpr int CW = 128 / BITS;
     constexpr int kThreads = kRowWaves * kWave;
     constexpr int kPlanes = T::bytes == 4 ? 2 : 1;
-    constexpr bool kOffset = offset_codes(BITS, T::bytes);
+    constexpr bool kOffset = offset_codes(T::bytes);
     extern __shared__ half8 xs[];                          // [token][plane][call][lane group]
     __shared__ unsigned top[kFewTokens];                   // largest magnitudes as bits (they are not negative)
     __shared__ floatx4 part[kRowWaves][kWave];
@@ -742,7 +758,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void linear_few(LinearArgs a, in
         for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor(sum[i], 8, kWave);
     }
     if (tok >= a.T || (kPlanes == 2 && n >= 8)) return;
-    finish4<T, offset_codes(BITS, T::bytes)>(a, tok, r0 + 4 * g, pow2(-row_exponent(__uint_as_float(top[tok]))), sum, par);
+    finish4<T, BITS>(a, tok, r0 + 4 * g, pow2(-row_exponent(__uint_as_float(top[tok]))), sum, par);
 }
 
 // ------------------------------------------------------------------- launches
@@ -765,7 +781,7 @@ bool few(int64_t T, int64_t K, int bits) { return T <= kFewTokens && T * padded(
 // are priced by the rounds they take, 2.8 fs for an output's column in a small
 // tile's round, and the joining of the parts at 5 TB/s.  Measured at 6144 -> 8192
 // in int4, bf16: 64 tokens 24 us small against 47 large, 256: 50 / 59, 512: 79 /
-// 84, 1024: 160 / 149, 4096: - / 449.
+// 84, 1024: 160 / 149, 4096: - / 449 (before the unsigned codes, 409 with them).
 struct Tiling {
     bool large;
     int splits;

@@ -9,8 +9,9 @@
 // (u = code + 8 at bit 0 or 4 of its half is u * 2^-24 or u * 2^-20; the 2^4 is
 // taken out of the query element that meets it, the offset out of the start of the
 // sum, which is -8 times the sum of the row's queries and as such the product's
-// free addend); the terms grow fourfold, the rounding of the fp32 sums with them,
-// far below that of the 16-bit result.  A row m is one query head of one
+// free addend); the matrix core loses the subnormals' leading zeros below the
+// largest product, 1e-5 of a sum's rms, far below the rounding of a 16-bit
+// result, and fp32 queries meet signed codes.  A row m is one query head of one
 // token; 16 rows that share a key/value head are the N side of the products
 // (B operand), 32 keys at a time the M side of S^T = K Q^T and the K side of
 // O^T = V^T P^T.  In S^T a lane holds one row (lane % 16) and, with the tokens

@@ -154,3 +154,16 @@ def test_two_streams_at_once():
             got.append(ops.linear(xd, lin))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in got)
+
+
+@pytest.mark.parametrize("bits", [4, 8, 2])
+@pytest.mark.parametrize("T", [5, 40, 300])
+def test_fp32_sums_keep_their_bits(T, bits):
+    """The error's rms, relative to the result's.  The pair drops 2^-22 of a
+    product; 2048 columns are 64 additions of 32 products to a partial sum whose rms
+    rises to the result's, each within a unit of its last place, 2^-23: at most
+    64 * 2^-23 + 2^-22 < 2^-16.9 in all, were they all one way."""
+    codes, scale, x, b, r = _case(T, 2048, 512, bits, "f32", False, False, seed=T + bits)
+    y = ops.linear(x.to(DEV), _lin(codes, scale, bits, None)).double().cpu().numpy()
+    want = aorc.linear(x.double().numpy(), codes, scale, None, "none", None)
+    assert np.sqrt(((y - want) ** 2).mean()) <= 2.0 ** -16.9 * np.sqrt((want ** 2).mean())
