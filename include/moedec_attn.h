@@ -56,8 +56,8 @@ extern "C" {
  * enters as an fp16 multiple of one power of two, so elements smaller than
  * 2^-23 of the row's largest lose bits), fp32 activations enter with about 22
  * bits; sums are fp32 (with 16-bit activations within about 1e-5 of their rms,
- * far below the rounding of y); y is rounded once.  A row of x that holds a NaN or an
- * infinity gives unspecified values in that row of y only.
+ * far below the rounding of y); y is rounded once.  A row of x that holds a NaN
+ * or an infinity gives unspecified values in that row of y only.
  * T == 0 is a no-op.  dense_linear_workspace gives -1 for sizes that are refused.
  * Requires K a positive multiple of 128/bits, N >= 1,
  * x and w 16-byte aligned, ldx*element size a multiple of 16, ldx >= K,

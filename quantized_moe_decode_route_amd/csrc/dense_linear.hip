@@ -547,11 +547,10 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join(LinearArgs a, const 
 // ------------------------------------------------------------- some tokens
 //
 // Up to TB * 16 tokens (64, 32 in fp32): bound by the weights' bytes and the planes'
-// L2 reads.  A
-// workgroup owns NB * 16 weight rows and all tokens; its waves split K by chunks
-// of 64 bytes of a row, all loads linear, kRowFlight chunks of codes in flight,
-// and meet in LDS in a fixed order.  37 bf16 tokens of 2048 -> 6144 in int8: 8.5 us
-// after 2.5 us of planes.
+// L2 reads.  A workgroup owns NB * 16 weight rows and all tokens; its waves split K
+// by chunks of 64 bytes of a row, all loads linear, kRowFlight chunks of codes in
+// flight, and meet in LDS in a fixed order.  37 bf16 tokens of 2048 -> 6144 in int8:
+// 8.5 us after 2.5 us of planes.
 constexpr int kRowWaves = 8;
 constexpr int kRowFlight = 4;               // even: the operands' two buffers alternate with it
 

@@ -25,8 +25,12 @@
 // it serves: NT = 1 for single tokens, 2 and 3 for drafts and prompts.  Bound by
 // HBM for few rows (each step's 32 * (head_dim + 8) bytes are loaded one step
 // ahead), by the vector ALUs for many (about 150 instructions a step for the
-// codes and 75 a row tile for the softmax, against 16 MFMAs of 16 cycles a row
-// tile at head_dim 128).
+// codes, fewer beside 16-bit queries, and 75 a row tile for the softmax, against 16
+// MFMAs of 16 cycles a row tile at head_dim 128).  At head_dim 128, 8 heads of keys
+// and 48 of queries: 64 sequences of up to 8192 keys, one bf16 query each, 80 + 5
+// us for 315 MB, 3.9 TB/s; 3 fp32 queries each of two sequences, up to 131,072 keys,
+// 101 + 7 us for 245 MB; 2813 bf16 queries of two sequences of up to 6000 keys 530
+// us, 636 TF/s.
 //
 // Queries enter as fp16 under one power of two per row: exact for fp16 and bf16,
 // as a hi/lo pair (22 bits) for fp32.  The probabilities times their value scale
@@ -585,7 +589,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_join(Cache c, AttnArgs
 
 // How a call is cut: 16-row blocks of a workgroup by the rows a sequence has on
 // average (prompts: three at head_dim 128, where four spilled registers, 614
-// against 587 us for 2 x 1500 queries of 48 heads over 6000 keys, now 530, and two
+// against 587 us for 2813 queries of 48 heads over up to 6000 keys, now 530, and two
 // elsewhere: at 64 two took 64 us for 3 x 1000 queries of 8 heads over 3000 keys,
 // three 70), and splits of the keys: enough workgroups for four
 // on every compute unit if the splits keep kMinChunk keys, and four times as many,

@@ -6,7 +6,8 @@
 // a NaN or an infinity s = NaN and codes 0.
 //
 // HBM- or latency-bound: 2 * head_dim elements read and head_dim + 8 bytes
-// written per row.  One wave owns the rows of an aligned block of 8 tokens, so
+// written per row (5601 bf16 tokens of 8 heads of 128: 16.5 us written, 1.8 TB/s, and
+// 13 read back; 42 tokens 3.9 us and 3.7, a launch and three memory latencies).  One wave owns the rows of an aligned block of 8 tokens, so
 // that every word of value codes (8 tokens of one column) is written whole by
 // one lane; a block that the call covers in part is read first and merged.
 // Blocks at a sequence's ends are the only ones written in part, and a page that
