@@ -129,7 +129,7 @@ __device__ __forceinline__ Tile find_tile(const Cache& c, const AttnArgs& a, int
     t.m = a.granted ? min(t.n, max(a.granted[t.s], 0)) : t.n;
     t.len = c.held(t.s);
     t.r0 = (slot - slot_base(a.q_start, t.s, a.rows, group, rt, 1)) * rt;
-    t.any = t.r0 < t.n * group;
+    t.any = t.r0 >= 0 && t.r0 < t.n * group;                                 // slots before the first sequence: none
     const int first = t.len - t.m + t.r0 / group;                            // position of the first row
     const int last = t.len - t.m + min(t.r0 + rt - 1, t.m * group - 1) / group;
     t.hi = t.r0 < t.m * group ? max(last + 1, 0) : 0;

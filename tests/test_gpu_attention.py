@@ -94,6 +94,29 @@ def test_granted():
     _check([40, 33, 64], [3, 2, 20], granted=[0, 2, 7])
 
 
+@pytest.mark.parametrize("lead", [1, 7, 40, 130])
+@pytest.mark.parametrize("news", [[1, 1, 1], [0, 3, 30], [70, 0, 9]])
+def test_rows_before_the_first_sequence(news, lead):
+    """q_start[0] > 0: rows of no sequence in front stay as they were, the others do
+    not notice them; one part and several, with and without heads that share.
+
+    The rows in front may change how the call is cut, so both results are within
+    their bound (_attn.attention_bound): with sum |q||k| / 8 below 32, values below
+    32 and at most 2000 keys that is 32 * (2 * 32 * (82 * 2^-24 + 2^-22) + 2^-18)
+    < 2^-6 each at the worst; rows mixed up would be off by their size."""
+    for heads, lens in ((4, [80, 33, 45]), (2, [2000, 40, 1200])):
+        rng = np.random.default_rng(lead)
+        cache = new_cache(lens)
+        fill(cache, lens, rng)
+        q = rows(rng, sum(news) + lead, heads, 64, "f32", strong=False).to(DEV)
+        st = starts(news)
+        want = ops.kv4_attention(q[lead:], cache, 0, ints(st))
+        out, lse = torch.full_like(q, 5.0), torch.full((q.shape[0], heads), 5.0, device=DEV)
+        ops.kv4_attention(q, cache, 0, ints([lead + a for a in st]), out=out, lse=lse)
+        assert (out[:lead] == 5).all() and (lse[:lead] == 5).all()
+        assert (out[lead:] - want).abs().max() <= 2.0 ** -5
+
+
 def test_positions_below_zero_are_empty():
     """More queries than tokens: the first ones see nothing."""
     _check([2, 5], [4, 5])

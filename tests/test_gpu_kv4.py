@@ -137,6 +137,21 @@ def test_rows_of_no_sequence_are_left_alone():
     assert torch.equal(cache.data, before)
 
 
+@pytest.mark.parametrize("lead", [1, 9, 100])
+def test_rows_before_the_first_sequence(lead):
+    lens = [20, 0, 45]
+    rng = np.random.default_rng(lead)
+    a, b = new_cache(lens), new_cache(lens)
+    b.data.copy_(a.data)
+    k, v = (rows(rng, lead + sum(lens), 2, 64, "f32").to(DEV) for _ in range(2))
+    ops.kv4_append(a, 0, k[lead:], v[lead:], ints(starts(lens)))
+    ops.kv4_append(b, 0, k, v, ints([lead + n for n in starts(lens)]))
+    assert torch.equal(a.data, b.data)
+    got = ops.kv4_read(b, 0, ints([0, 0, 0]), ints([lead + n for n in starts(lens)]), lead + sum(lens))
+    for x, y in zip(got, _read(a, lens)):
+        assert torch.equal(x[lead:], y)
+
+
 def test_many_sequences():
     """The 64-way search over sequences, with empty ones between."""
     rng = np.random.default_rng(11)
