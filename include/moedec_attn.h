@@ -47,7 +47,7 @@ extern "C" {
  *   w        : uint8 [N, K*bits/8] packed codes in the layout of moe_pack_q*
  *   scale    : fp32 [N]; bias: fp32 [N] or NULL
  *   residual : [T] rows of N elements of `dtype`, ldr apart, or NULL; may be y
- *              itself (with ldr == ldy)
+ *              itself (with ldr == ldy), else must not overlap it
  *   y        : [T] rows of N elements of `dtype`, ldy apart; must not overlap x
  *   workspace: dense_linear_workspace(...) bytes of device memory,
  *              16-byte aligned (NULL when that is 0); calls that may run at
@@ -61,7 +61,8 @@ extern "C" {
  * T == 0 is a no-op.  dense_linear_workspace gives -1 for sizes that are refused.
  * Requires K a positive multiple of 128/bits, N >= 1,
  * x and w 16-byte aligned, ldx*element size a multiple of 16, ldx >= K,
- * ldr, ldy >= N (INVALID_ARG); K <= 65536, T and N < 2^24 and T*N/512 < 2^31
+ * ldr, ldy >= N, no overlap but the one above (INVALID_ARG; rows of one stride
+ * may interleave, as columns of one buffer do); K <= 65536, T and N < 2^24 and T*N/512 < 2^31
  * (UNSUPPORTED).
  */
 int64_t dense_linear_workspace(int bits, int dtype, int64_t T, int64_t K, int64_t N);
@@ -138,7 +139,7 @@ int kv4_read(const kv4_cache* cache, int layer, const int32_t* first, const int3
  * keys j of the row's sequence with j <= pos(r) and, if window > 0, j > pos(r) -
  * window; head h reads key/value head h / (heads / kv_heads).
  *   q, out  : [rows][heads][head_dim] of `dtype`, row strides ldq, ldo; out must
- *             not overlap q
+ *             not overlap q (INVALID_ARG; columns of one buffer may interleave)
  *   lse     : fp32 [rows][heads] or NULL; the natural log of sum_j
  *             exp(scale * q . k_j)
  *   max_len : an upper bound of the lengths as far as the caller knows it

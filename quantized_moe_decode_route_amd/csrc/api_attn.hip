@@ -50,6 +50,18 @@ int check_cache(const kv4_cache* c, Cache& out) {
 
 bool stride_ok(int64_t ld, int64_t row, int dtype) { return ld >= row && ld * dtype_bytes(dtype) % 16 == 0; }
 
+// Whether rows of wa elements lda apart and rows of wb elements ldb apart share an
+// element.  Rows of one stride may interleave (columns of one buffer); others
+// count as shared where their ranges meet.
+bool overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows,
+             int64_t bytes) {
+    const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a), pb = (int64_t)reinterpret_cast<uintptr_t>(b);
+    if (pa + ((rows - 1) * lda + wa) * bytes <= pb || pb + ((rows - 1) * ldb + wb) * bytes <= pa) return false;
+    if (rows == 1 || lda != ldb) return true;
+    const int64_t ld = lda * bytes, d = ((pb - pa) % ld + ld) % ld;
+    return d < wa * bytes || d + wb * bytes > ld;
+}
+
 int check_rows(const Cache& c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype,
                int64_t rows, const int32_t* q_start) {
     if (!q_start || !aligned4(q_start) || layer < 0 || layer >= c.layers || rows < 0 || !dtype_ok(dtype))
@@ -84,6 +96,10 @@ int linear(int bits, const void* x, int dtype, int64_t ldx, const uint8_t* w, co
     if ((reinterpret_cast<uintptr_t>(y) & e) || (reinterpret_cast<uintptr_t>(residual) & e))
         return MOEDEC_ERR_INVALID_ARG;
     if (K > 65536 || T >= kMaxRows || N >= kMaxRows) return MOEDEC_ERR_UNSUPPORTED;
+    const int64_t bytes = dtype_bytes(dtype);
+    if (overlap(x, ldx, K, y, ldy, N, T, bytes)) return MOEDEC_ERR_INVALID_ARG;
+    if (residual && (residual != y || (ldr != ldy && T > 1)) && overlap(residual, ldr, N, y, ldy, N, T, bytes))
+        return MOEDEC_ERR_INVALID_ARG;
     const int64_t need = linear_workspace(bits, dtype, T, K, N);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return MOEDEC_ERR_INVALID_ARG;
     LinearArgs a;
@@ -169,6 +185,7 @@ MOEDEC_API int kv4_attention(const kv4_cache* cache, int layer, const void* q, i
     const int64_t row = (int64_t)heads * c.head_dim;
     if (!q || !out || !aligned16(q) || !aligned16(out) || !stride_ok(ldq, row, dtype) || !stride_ok(ldo, row, dtype))
         return MOEDEC_ERR_INVALID_ARG;
+    if (overlap(q, ldq, row, out, ldo, row, rows, dtype_bytes(dtype))) return MOEDEC_ERR_INVALID_ARG;
     const int64_t need = attention_workspace(c, (int)rows, heads, max_len);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return MOEDEC_ERR_INVALID_ARG;
     AttnArgs a;

@@ -132,6 +132,30 @@ def test_bad_linear(lib, bits):
         assert lib.dense_linear_workspace(*sizes) == -1
 
 
+def test_overlaps(lib):
+    """Outputs over inputs are refused (that columns of one buffer are not, the GPU
+    tests show)."""
+    need = lib.dense_linear_workspace(4, 0, 300, 128, 64)
+
+    def linear(y, ldy, res=None, ldr=0, ldx=128, nb=need - 1, T=300):
+        return lib.dense_linear_q4(FAKE, 0, ldx, FAKE + (1 << 24), FAKE, None, 0, res, ldr, y, ldy, T, 128, 64, FAKE,
+                                   nb, None)
+
+    assert need > 0
+    for y, ldy in ((FAKE, 64), (FAKE + 4 * 128 * 299, 64), (FAKE + 4 * 64, 128), (FAKE - 4 * 63, 256)):
+        assert linear(y, ldy, nb=need, ldx=256 if ldy == 256 else 128) == 1, (y - FAKE, ldy)
+    far = FAKE + (1 << 23)
+    for res, ldr in ((far + 4, 64), (far - 4, 64), (far, 80)):
+        assert linear(far, 64, res, ldr, nb=need) == 1, (res - far, ldr)
+    c = ctypes.byref(_cache())
+
+    def attend(out, rows=4, ldq=512, ldo=512, ws=None, nb=0):
+        return lib.kv4_attention(c, 0, FAKE, ldq, 0, rows, 4, FAKE, None, 1.0, 0, 64, out, ldo, None, ws, nb, None)
+
+    for out, ld in ((FAKE, 512), (FAKE + 4 * 252, 512), (FAKE - 4 * 252, 512), (FAKE + 4 * 256 * 3, 256)):
+        assert attend(out, ldq=ld, ldo=ld) == 1, (out - FAKE, ld)
+
+
 def test_binding_refuses(lib):
     x = torch.zeros((2, 128))
     lin = ops.Linear(torch.zeros((8, 64), dtype=torch.uint8), torch.zeros(8), 4)

@@ -299,6 +299,19 @@ def test_long_flat_cache():
         assert (np.abs(out - o) <= loose + mag * (6 * p / np.sqrt(n) + 2.0 ** -17)).all()
 
 
+def test_output_beside_and_over_queries():
+    lens, news = [50, 20], [3, 1]
+    cache = new_cache(lens)
+    fill(cache, lens, np.random.default_rng(0))
+    buf = torch.randn(4, 8, 64, device=DEV)
+    want = ops.kv4_attention(buf[:, :4].contiguous(), cache, 0, ints(starts(news)))
+    ops.kv4_attention(buf[:, :4], cache, 0, ints(starts(news)), out=buf[:, 4:])
+    assert torch.equal(buf[:, 4:], want)
+    for bad in (buf[:, :4], buf[:, 2:6]):
+        with pytest.raises(ops.MoedecError):
+            ops.kv4_attention(buf[:, :4], cache, 0, ints(starts(news)), out=bad)
+
+
 def test_binding_refuses():
     cache = new_cache([4], 32)
     q, start = torch.zeros((1, 4, 64), device=DEV), ints([0, 1])

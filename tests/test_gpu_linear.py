@@ -167,3 +167,19 @@ def test_fp32_sums_keep_their_bits(T, bits):
     y = ops.linear(x.to(DEV), _lin(codes, scale, bits, None)).double().cpu().numpy()
     want = aorc.linear(x.double().numpy(), codes, scale, None, "none", None)
     assert np.sqrt(((y - want) ** 2).mean()) <= 2.0 ** -16.9 * np.sqrt((want ** 2).mean())
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_columns_of_one_buffer(T):
+    """x, residual and out may be columns of one buffer; out over x is refused."""
+    codes, scale, x, b, r = _case(T, 128, 64, 4, "f32", True, True, seed=T)
+    lin, buf = _lin(codes, scale, 4, b), torch.zeros(T, 256, device=DEV)
+    buf[:, :128], buf[:, 192:] = x.to(DEV), r.to(DEV)
+    want = ops.linear(x.to(DEV), lin, residual=r.to(DEV))
+    ops.linear(buf[:, :128], lin, residual=buf[:, 192:], out=buf[:, 128:192])
+    assert torch.equal(buf[:, 128:192], want) and torch.equal(buf[:, :128].cpu(), x)
+    for bad in (buf[:, 64:128], buf[:, 96:160]):
+        with pytest.raises(ops.MoedecError):
+            ops.linear(buf[:, :128], lin, out=bad)
+    with pytest.raises(ops.MoedecError):
+        ops.linear(x.to(DEV), lin, residual=buf[:, 4:68], out=buf[:, :64])
